@@ -22,3 +22,4 @@ from .binding import (  # noqa: F401
     upload_layer,
     workspace_bytes,
 )
+from .kvcache import KV_EXPORTED, KVCache, kv_desc, kv_workspace_bytes  # noqa: F401

@@ -19,34 +19,43 @@
 #include <cstdint>
 #include <cstdio>
 #include <new>
-#include <string>
 
 #include "kernels.h"
 #include "pi_ffn.h"
+#include "status.h"
 
 #include <mutex>
 
 // The workspace of pi_ffn_forward_static (see static_scratch below).
 static __device__ __align__(256) char scratch[PI_FFN_STATIC_SCRATCH_BYTES];
 
-namespace {
+namespace pik {
 
-thread_local std::string g_last_error;
+namespace {
+thread_local char g_last_error[512];
+}  // namespace
 
 pi_status fail(pi_status st, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return st;
 }
 
 pi_status ok() {
-  g_last_error.clear();
+  g_last_error[0] = 0;
   return PI_OK;
 }
+
+const char* last_error() { return g_last_error; }
+
+}  // namespace pik
+
+namespace {
+
+using pik::fail;
+using pik::ok;
 
 constexpr size_t kAlign = 256;
 constexpr int kMaxBatch = pik::kMaxBatchTokens;
@@ -414,7 +423,7 @@ extern "C" {
 
 int32_t pi_ffn_abi_version(void) { return PI_FFN_ABI_VERSION; }
 
-const char* pi_last_error(void) { return g_last_error.c_str(); }
+const char* pi_last_error(void) { return pik::last_error(); }
 
 pi_status pi_ffn_workspace_bytes(const pi_ffn_desc* desc, size_t* bytes) {
   pi_status st = check_desc(desc);

@@ -1,0 +1,74 @@
+// Host-side launch interface of the attention cache's kernels (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace pik {
+
+constexpr int kKvBlock = 32;   // tokens that share an exponent
+
+// One layer of the cache and the call's sequences, as every token kernel takes them (by value).
+struct KvView {
+  uint8_t* k;          // the layer's codes [pages][kv_heads][blocks a page][32 * D]
+  uint8_t* v;
+  uint8_t* k_exp;      // [pages][kv_heads][blocks a page]
+  uint8_t* v_exp;
+  const int* table;    // [max_seqs][max_pages]
+  const int* lens;     // [max_seqs]
+  const int* seqs;     // [n]
+  const int* starts;   // [n + 1]
+  int n, rows;
+  int kv_heads, dim, page_blocks;   // page_blocks: blocks a page
+  int pages, max_seqs, max_pages;
+};
+
+// A packed tensor [rows][heads][D] of the activations' type: strides in elements.
+struct KvRows {
+  void* data;
+  int64_t token, head;
+};
+
+struct KvStoreArgs {
+  KvView c;
+  KvRows k, v;
+  const int* first;    // read: first token of each sequence, or NULL
+};
+hipError_t launch_kv_append(int act, int code, const KvStoreArgs& a, hipStream_t s);
+hipError_t launch_kv_read(int act, int code, const KvStoreArgs& a, hipStream_t s);
+
+struct KvAttendArgs {
+  KvView c;
+  KvRows q, out;
+  float* lse;          // [rows][heads] or NULL
+  int heads, group;    // group: query heads of a cached head
+  int max_new, window, sinks;
+  float scale;
+};
+hipError_t launch_kv_attend(int act, int code, const KvAttendArgs& a, hipStream_t s);
+
+// The pool as the page kernels take it.
+struct KvPool {
+  uint8_t* k;          // [layers][pages][k_bytes]
+  uint8_t* v;
+  uint8_t* k_exp;      // [layers][pages][e_bytes]
+  uint8_t* v_exp;
+  int* table;
+  int* lens;
+  int* refs;
+  int* failed;
+  int* src;            // workspace: pages to copy from and to, -1 for none [max(pages, max_seqs)]
+  int* dst;
+  int* list;           // workspace: reserve's free pages, compact's new places [pages]
+  int* count;          // workspace: how many copies
+  int64_t page_bytes;  // of k and of v
+  int exp_bytes;       // a page's exponents, of k and of v
+  int pages, layers, max_seqs, max_pages, page_tokens;
+};
+hipError_t launch_kv_free(const KvPool& p, const int* seqs, int n, hipStream_t s);
+hipError_t launch_kv_fork(const KvPool& p, const int* src, const int* dst, int n, hipStream_t s);
+hipError_t launch_kv_reserve(const KvPool& p, const int* seqs, const int* counts, int n, hipStream_t s);
+hipError_t launch_kv_compact(const KvPool& p, hipStream_t s);
+
+}  // namespace pik

@@ -37,3 +37,17 @@ from .ffn import (  # noqa: F401
     threshold_logit,
     union_mask,
 )
+from .kv import (  # noqa: F401
+    KV_BLOCK,
+    KV_MAX,
+    KvModel,
+    kv_attend,
+    kv_clean,
+    kv_compact,
+    kv_exponent,
+    kv_fork,
+    kv_free,
+    kv_reserve,
+    kv_round,
+    kv_visible,
+)
