@@ -45,8 +45,21 @@ struct KvAttendArgs {
   int heads, group;    // group: query heads of a cached head
   int max_new, window, sinks;
   float scale;
+  int slots, splits;   // set by the launch of many rows
+  float* partial;      // workspace: step_partial_floats(D) or tile_partial_floats(D) floats
+  unsigned* tickets;   // workspace: kStepGroups counters, zero between calls
 };
-hipError_t launch_kv_attend(int act, int code, const KvAttendArgs& a, hipStream_t s);
+
+// Few rows of a cached head (max_new * group up to kStepRows): kStepGroups workgroups, two a compute unit,
+// each with an equal stretch of the call's blocks, in grains of kStepGrain.
+constexpr int kStepRows = 64, kStepGroups = 512, kStepGrain = 8;
+constexpr size_t step_partial_floats(int dim) { return (size_t)2 * kStepGroups * kStepRows * (dim + 4); }
+hipError_t launch_kv_step(int act, int code, const KvAttendArgs& a, hipStream_t s);
+// Any number of rows, kTileRows a workgroup; where that leaves fewer than kTileParts / 2 workgroups, the
+// tokens of each are split over up to kTileParts in all.
+constexpr int kTileRows = 128, kTileParts = 512;
+constexpr size_t tile_partial_floats(int dim) { return (size_t)kTileParts * kTileRows * (dim + 4); }
+hipError_t launch_kv_tile(int act, int code, const KvAttendArgs& a, hipStream_t s);
 
 // The pool as the page kernels take it.
 struct KvPool {

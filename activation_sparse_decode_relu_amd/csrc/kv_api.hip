@@ -1,6 +1,7 @@
 // C ABI of the attention cache: argument checks, workspace layout and the kernels of each call.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -22,17 +23,20 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 struct Layout {
-  size_t src, dst, list, count, total;
+  size_t tickets, count, src, dst, list, partial, total;
 };
 
 Layout layout_for(const pi_kv_desc& d) {
   Layout L{};
   const size_t copies = (size_t)(d.pages > d.max_seqs ? d.pages : d.max_seqs);
   size_t off = 0;
+  L.tickets = off; off = align_up(off + pik::kStepGroups * sizeof(unsigned));
   L.count = off; off = align_up(off + 2 * sizeof(int));
   L.src = off;   off = align_up(off + copies * sizeof(int));
   L.dst = off;   off = align_up(off + copies * sizeof(int));
   L.list = off;  off = align_up(off + (size_t)d.pages * sizeof(int));
+  L.partial = off; off = align_up(off + std::max(pik::step_partial_floats(d.head_dim),
+                                              pik::tile_partial_floats(d.head_dim)) * sizeof(float));
   L.total = off;
   return L;
 }
@@ -256,7 +260,18 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
   a.window = args->window;
   a.sinks = args->sinks;
   a.scale = args->scale;
-  return launched(pik::launch_kv_attend(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
+  a.partial = reinterpret_cast<float*>(h->ws + h->L.partial);
+  a.tickets = reinterpret_cast<unsigned*>(h->ws + h->L.tickets);
+  if ((int64_t)a.max_new * a.group <= pik::kStepRows) {
+    // the kernel counts the call's blocks of 32 tokens in 32 bits
+    const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
+    const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + a.max_new) / PI_KV_BLOCK + 4) : cap;
+    if ((seen + pik::kStepGrain) * a.c.kv_heads * a.c.n > INT32_MAX)
+      return fail(PI_ERR_UNSUPPORTED, "%d sequences of up to %lld blocks and %d heads are more than one call takes", a.c.n,
+                  (long long)seen, a.c.kv_heads);
+    return launched(pik::launch_kv_step(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
+  }
+  return launched(pik::launch_kv_tile(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
 }
 
 pi_status pi_kv_reserve(pi_kv* h, const int32_t* seqs, const int32_t* counts, int32_t n, void* stream) {

@@ -1,0 +1,388 @@
+// Attention of few rows: single tokens and a handful (up to 64 rows of a cached head), over long caches.
+//
+// Bound by reading the codes, so the split is over bytes.  The call's blocks of 32 tokens, over all
+// sequences and cached heads, stand in one line; each of a fixed number of workgroups takes an equal
+// stretch of it, whatever the lengths are, and works out its stretch itself from the lengths (they
+// are on the device).  The four waves of a workgroup take the blocks of a stretch in turn, each with its
+// own online softmax, straight from memory to the matrix instructions' operands: a block's bytes are stored
+// in their order, so each load is one contiguous KB and nothing passes through LDS.  One
+// 16x16x32 tile holds up to 16 rows: all query heads of a cached head, for all its new tokens.
+//
+// A sequence and head that lies in one stretch is finished by its workgroup; otherwise each workgroup leaves
+// its state (fp32) in the workspace and the last of them, by a ticket, joins the parts in their order,
+// so the result does not depend on who was last.
+#include "kv_softmax.h"
+
+namespace pik {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+// What one sequence brings to the line, as a lane holds it.
+struct StepSeq {
+  int seq, len, row0, rows;   // rows: those computed, at most max_new
+  int p0;                     // position of its first row
+  int blocks;                 // visible blocks, at least 1
+  int units;                  // places in the line: kv_heads * (blocks rounded up to kStepGrain)
+};
+
+__device__ __forceinline__ int grain_up(int blocks) { return (blocks + kStepGrain - 1) / kStepGrain * kStepGrain; }
+
+__device__ __forceinline__ StepSeq step_seq(const KvAttendArgs& A, int i) {
+  StepSeq r{-1, 0, 0, 0, 0, 1, 0};
+  if (i >= A.c.n) return r;
+  const KvSeq s = kv_seq(A.c, i);
+  r.seq = s.seq;
+  r.len = s.len;
+  r.row0 = s.row0;
+  r.rows = min(s.rows, A.max_new);
+  r.p0 = s.len - s.rows;
+  if (r.rows > 0) {
+    r.blocks = max(span_of(r.p0, r.p0 + r.rows - 1, A.window, A.sinks).count(), 1);
+    r.units = grain_up(r.blocks) * A.c.kv_heads;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+__device__ __forceinline__ int wave_total(int v) {
+#pragma unroll
+  for (int m = 1; m < WAVE; m <<= 1) v += __shfl_xor(v, m);
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+__device__ __forceinline__ int wave_inclusive(int v) {
+  const int lane = threadIdx.x & (WAVE - 1);
+#pragma unroll
+  for (int off = 1; off < WAVE; off <<= 1) {
+    const int y = __shfl_up(v, off, WAVE);
+    if (lane >= off) v += y;
+  }
+  return v;
+}
+
+// The codes of one block, as a wave loads them.
+template <int D> struct Codes {
+  u32x4 k[D / 32], v[D / 32];
+};
+
+template <int D>
+__device__ __forceinline__ void load_codes(Codes<D>& c, const uint8_t* k, const uint8_t* v) {
+  const int lane = threadIdx.x & (WAVE - 1);
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) c.k[q] = ld_stream(reinterpret_cast<const u32x4*>(k + q * 1024) + lane);
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) c.v[q] = ld_stream(reinterpret_cast<const u32x4*>(v + q * 1024) + lane);
+}
+
+template <int ACT, int CODE, int D, int NT>
+__global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k_kv_step(const KvAttendArgs A) {
+  using T = typename ActT<ACT>::T;
+  using V8 = typename ActT<ACT>::V8;
+  constexpr int kRows = 16 * NT, kRow = D + 4;        // rows of a tile; floats of a row's partial
+  __shared__ float s_part[kWaves][kRows][kRow];       // O', then rr, mm, l
+  __shared__ int s_last;
+  const KvView& c = A.c;
+  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int g = lane >> 4, col = lane & 15;
+  const __amdgpu_buffer_rsrc_t prs = partial_rsrc(A.partial);
+
+  // ---- this workgroup's stretch of the line --------------------------------------------------------
+  StepSeq mine = step_seq(A, lane);
+  int total = mine.units;
+  for (int base = WAVE; base < c.n; base += WAVE) total += step_seq(A, base + lane).units;
+  total = wave_total(total);
+  // equal shares, in whole grains
+  const int share = grain_up((int)(((long long)total + gridDim.x - 1) / gridDim.x));
+  const int begin = (int)min((long long)blockIdx.x * share, (long long)total);
+  const int end = min(begin + share, total);
+  if (begin >= end) return;
+  int base = 0, before = 0;                           // the 64 sequences in `mine`, and the units before them
+  int incl = wave_inclusive(mine.units);
+  while (before + lane_of(incl, WAVE - 1) <= begin) {
+    before += lane_of(incl, WAVE - 1);
+    base += WAVE;
+    mine = step_seq(A, base + lane);
+    incl = wave_inclusive(mine.units);
+  }
+  int at = __builtin_ctzll(__ballot(before + incl > begin));   // lane of the sequence that holds `begin`
+
+  for (int u = begin; u < end;) {
+    if (at == WAVE || before + lane_of(incl, WAVE - 1) <= u) {
+      before += lane_of(incl, WAVE - 1);
+      base += WAVE;
+      mine = step_seq(A, base + lane);
+      incl = wave_inclusive(mine.units);
+      at = __builtin_ctzll(__ballot(before + incl > u));
+    }
+    const int seq = lane_of(mine.seq, at), len = lane_of(mine.len, at), row0 = lane_of(mine.row0, at);
+    const int nrows = lane_of(mine.rows, at), p0 = lane_of(mine.p0, at), units = lane_of(mine.units, at);
+    const int blocks = lane_of(mine.blocks, at), first_unit = before + lane_of(incl, at) - units;
+    if (units == 0 || u >= first_unit + units) {
+      ++at;
+      continue;
+    }
+    const int cost = grain_up(blocks), head = (u - first_unit) / cost;
+    const int item = first_unit + head * cost;        // where this sequence and head begins in the line
+    const int b0 = u - item, b1 = min(min(cost, b0 + end - u), blocks);
+    const int next = min(item + cost, end);
+    const int p1 = p0 + nrows - 1, R = nrows * A.group;
+    Span span = span_of(p0, p1, A.window, A.sinks);
+    if (seq < 0) span = Span{0, 0, 0};
+    const int inv_group = (65536 + A.group - 1) / A.group;   // r / group for r < 128: r * inv_group >> 16
+
+    // ---- the rows: row 16 t + col of the tile, dims (4 (s / 2) + g) 16 + 8 (s % 2) .. + 8 in step s ----
+    f16x8 q[NT][D / 32];
+    float row_mul[NT];
+    int pos[NT];
+    RowState st[NT];
+    f32x4 o[NT][D / 16];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = 16 * t + col;
+      const int j = (r * inv_group) >> 16, hh = r - j * A.group;
+      const bool live = r < R;
+      pos[t] = live ? p0 + j : -1;
+      const T* src = static_cast<const T*>(A.q.data) + (int64_t)(row0 + (live ? j : 0)) * A.q.token +
+                     (int64_t)(head * A.group + (live ? hh : 0)) * A.q.head;
+      V8 x[D / 32];
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+        x[s] = V8{};
+        if (live) x[s] = *reinterpret_cast<const V8*>(src + (4 * (s / 2) + g) * 16 + 8 * (s % 2));
+      }
+      float up = 1.0f, down = 1.0f;
+      if constexpr (ACT == ACT_BF16) {
+        float m = 0.0f;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) m = fmaxf(m, max8<ACT>(x[s]));
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        up = query_scale(m, down);
+      }
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) q[t][s] = query8<ACT>(x[s], up);
+      row_mul[t] = A.scale * kLog2e * down;
+      st[t] = RowState{-INFINITY, -INFINITY, 0.0f};
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // ---- this wave's blocks: b0 + wave, + kWaves, ... ------------------------------------------------
+    const int count = b1 - b0 > wave ? (b1 - b0 - wave + kWaves - 1) / kWaves : 0;
+    for (int k0 = 0; k0 < count; k0 += WAVE) {
+      // where 64 of them lie: lane k holds block k0 + k
+      int page = -1, slot = 0, blk = 0, exps = 0;
+      const int m = min(count - k0, WAVE);
+      if (lane < m) {
+        const int bi = b0 + wave + (k0 + lane) * kWaves;
+        if (bi < span.count()) {
+          blk = span.block(bi);
+          page = kv_page(c, seq, blk);
+          slot = blk % c.page_blocks;
+        }
+        if (page >= 0) {
+          const size_t e = block_at(c, page, head, slot);
+          exps = (int)c.k_exp[e] | (int)c.v_exp[e] << 8;
+        }
+      }
+      Codes<D> cur, nxt;
+      auto fetch = [&](int k, Codes<D>& to) {
+        const size_t e = block_at(c, max(lane_of(page, k), 0), head, lane_of(slot, k)) * (kKvBlock * D);
+        load_codes<D>(to, c.k + e, c.v + e);
+      };
+      fetch(0, cur);
+      for (int k = 0; k < m; ++k) {
+        if (k + 1 < m) fetch(k + 1, nxt);
+        const int t0 = lane_of(blk, k) * kKvBlock;
+        if (lane_of(page, k) >= 0) {
+          const int ex = lane_of(exps, k);
+          const int ek = max((ex & 255) - 127, -126), ev = max((ex >> 8) - 127, -126);
+          const float evf = (float)ev;
+          // scores: register 4 t + i of the lane is token t0 + 8 g + 4 t + i
+          float s[NT][8];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            f16x8 a[D / 32];
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w) {
+              const u32x4 x = cur.k[t * (D / 64) + w];
+              a[2 * w] = decode8<CODE>(x.x, x.y);
+              a[2 * w + 1] = decode8<CODE>(x.z, x.w);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int w = 0; w < D / 32; ++w)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[w], q[n][w], acc, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[i];
+            }
+          }
+          // every row sees the whole block unless it reaches past the first row or before a window
+          if (t0 + kKvBlock - 1 > p0 || (A.window > 0 && t0 <= p1 - A.window)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                s[n][j] = row_sees(pos[n], t0 + 8 * g + j, A.window, A.sinks) ? s[n][j] : -INFINITY;
+            // codes past the end are whatever the memory held
+            const int left = min(max(len - (t0 + 8 * g), 0), 8);
+            const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+            const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
+#pragma unroll
+            for (int p = 0; p < D / 32; ++p) cur.v[p] &= u32x4{lo, hi, lo, hi};
+          }
+          float mul[NT], top[NT];
+          bool move = false;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mul[n] = score_factor(row_mul[n], ek);
+            top[n] = s[n][0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) top[n] = fmaxf(top[n], s[n][j]);
+            top[n] *= mul[n];
+            move |= passes(st[n], top[n], evf);
+          }
+          if (__any(move)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float x = fmaxf(top[n], __shfl_xor(top[n], 16));
+              x = fmaxf(x, __shfl_xor(x, 32));
+              const float f = move_refs(st[n], x, evf);
+#pragma unroll
+              for (int d = 0; d < D / 16; ++d) o[n][d] *= f;
+            }
+          }
+          f16x8 w[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) weigh<8>(st[n], s[n], mul[n], evf, &w[n]);
+#pragma unroll
+          for (int p = 0; p < D / 32; ++p) {
+            const f16x8 a = decode8<CODE>(cur.v[p].x, cur.v[p].y), b = decode8<CODE>(cur.v[p].z, cur.v[p].w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[n][2 * p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[n], o[n][2 * p], 0, 0, 0);
+              o[n][2 * p + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, w[n], o[n][2 * p + 1], 0, 0, 0);
+            }
+          }
+        }
+        if (k + 1 < m) cur = nxt;
+      }
+    }
+
+    // ---- join the waves: the row's state and O' through LDS -------------------------------------------
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float l = st[n].l;
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      float* to = s_part[wave][16 * n + col];
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4*>(to + 16 * d + 4 * g) = o[n][d];
+      if (g == 0) *reinterpret_cast<f32x4*>(to + D) = f32x4{st[n].rr, st[n].mm, l, 0.f};
+    }
+    __syncthreads();
+    const bool whole = b0 == 0 && item + cost <= end;
+    const int first = item / share, last = (item + cost - 1) / share;   // the workgroups it is spread over
+    const int part = 2 * (int)blockIdx.x + ((int)blockIdx.x == first ? 1 : 0);
+    for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
+      const int r = k / (D / 4), d = 4 * (k % (D / 4));
+      RowState a{-INFINITY, -INFINITY, 0.0f};
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const f32x4 b = *reinterpret_cast<const f32x4*>(&s_part[w][r][D]);
+        float fa, fb;
+        join(a, RowState{b.x, b.y, b.z}, fa, fb);
+        v = v * fa + *reinterpret_cast<const f32x4*>(&s_part[w][r][d]) * fb;
+      }
+      if (!whole) {
+        const int to = (part * kRows + r) * kRow;
+        put4(prs, to + d, v);
+        if (d == 0) put4(prs, to + D, f32x4{a.rr, a.mm, a.l, 0.f});
+        continue;
+      }
+      const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
+      T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
+      const float half = out_half(a);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
+      if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
+    }
+    if (!whole) {
+      // every wave's partial stores are complete before the barrier, the ticket is drawn after it
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (threadIdx.x == 0)
+        s_last = __hip_atomic_fetch_add(A.tickets + first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 (unsigned)(last - first);
+      __syncthreads();
+      if (s_last) {
+        for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
+          const int r = k / (D / 4), d = 4 * (k % (D / 4));
+          RowState a{-INFINITY, -INFINITY, 0.0f};
+          f32x4 v = {0.f, 0.f, 0.f, 0.f};
+          for (int p = first; p <= last; p += 4) {
+            f32x4 x[4], y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int from = ((2 * min(p + e, last) + (p + e == first ? 1 : 0)) * kRows + r) * kRow;
+              x[e] = get4(prs, from + D);
+              y[e] = get4(prs, from + d);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (p + e <= last) {
+                float fa, fb;
+                join(a, RowState{x[e].x, x[e].y, x[e].z}, fa, fb);
+                v = v * fa + y[e] * fb;
+              }
+          }
+          const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
+          T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
+          const float half = out_half(a);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
+          if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
+        }
+        if (threadIdx.x == 0) __hip_atomic_store(A.tickets + first, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    __syncthreads();   // s_part is free again
+    u = next;
+  }
+}
+
+template <int ACT, int CODE, int D, int NT>
+hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(kStepGroups), dim3(WAVE * kWaves), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int ACT, int CODE, int D>
+hipError_t step_rows(const KvAttendArgs& a, hipStream_t s) {
+  const int rows = a.max_new * a.group;
+  if (rows <= 16) return step_go<ACT, CODE, D, 1>(a, s);
+  if (rows <= 32) return step_go<ACT, CODE, D, 2>(a, s);
+  return step_go<ACT, CODE, D, 4>(a, s);
+}
+
+template <int ACT>
+hipError_t step_code(int code, const KvAttendArgs& a, hipStream_t s) {
+  if (code == CODE_E4M3)
+    return a.c.dim == 128 ? step_rows<ACT, CODE_E4M3, 128>(a, s) : step_rows<ACT, CODE_E4M3, 64>(a, s);
+  return a.c.dim == 128 ? step_rows<ACT, CODE_INT8, 128>(a, s) : step_rows<ACT, CODE_INT8, 64>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_kv_step(int act, int code, const KvAttendArgs& a, hipStream_t s) {
+  if (a.max_new < 1 || (long long)a.max_new * a.group > kStepRows) return hipErrorInvalidValue;
+  return act == ACT_F16 ? step_code<ACT_F16>(code, a, s) : step_code<ACT_BF16>(code, a, s);
+}
+
+}  // namespace pik
