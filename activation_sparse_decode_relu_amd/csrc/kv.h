@@ -47,13 +47,21 @@ struct KvAttendArgs {
   float scale;
   int slots, splits;   // set by the launch of many rows
   float* partial;      // workspace: step_partial_floats(D) or tile_partial_floats(D) floats
-  unsigned* tickets;   // workspace: kStepGroups counters, zero between calls
+  unsigned* tickets;   // workspace: kStepTickets counters, zero between calls
 };
 
-// Few rows of a cached head (max_new * group up to kStepRows): kStepGroups workgroups, two a compute unit,
-// each with an equal stretch of the call's blocks, in grains of kStepGrain.
-constexpr int kStepRows = 64, kStepGroups = 512, kStepGrain = 8;
-constexpr size_t step_partial_floats(int dim) { return (size_t)2 * kStepGroups * kStepRows * (dim + 4); }
+// Few rows of a cached head (max_new * group up to kStepRows): step_groups workgroups, as many as the card holds
+// at once, each with an equal stretch of the call's blocks, in grains of kStepGrain.
+constexpr int kStepRows = 64, kStepGrain = 8;
+// tiles: 16-row tiles a wave holds.  Two to four workgroups a compute unit, by the registers these take.
+constexpr int step_groups(int tiles, int dim) {
+  return 256 * (tiles == 1 ? (dim == 64 ? 4 : 3) : tiles == 4 && dim == 128 ? 1 : 2);
+}
+constexpr int kStepTickets = 2 * 1024;
+// a workgroup leaves two parts at most: of the item it starts in and of the one it ends in
+constexpr size_t step_partial_floats(int dim) { return (size_t)2 * 512 * kStepRows * (dim + 4); }
+static_assert(step_groups(1, 64) * 16 <= 512 * kStepRows && step_groups(1, 128) * 16 <= 512 * kStepRows &&
+              step_groups(2, 64) * 32 <= 512 * kStepRows && step_groups(1, 64) <= kStepTickets / 2, "workspace");
 hipError_t launch_kv_step(int act, int code, const KvAttendArgs& a, hipStream_t s);
 // Any number of rows, kTileRows a workgroup; where that leaves fewer than kTileParts / 2 workgroups, the
 // tokens of each are split over up to kTileParts in all.

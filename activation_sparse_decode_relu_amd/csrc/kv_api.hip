@@ -30,7 +30,7 @@ Layout layout_for(const pi_kv_desc& d) {
   Layout L{};
   const size_t copies = (size_t)(d.pages > d.max_seqs ? d.pages : d.max_seqs);
   size_t off = 0;
-  L.tickets = off; off = align_up(off + pik::kStepGroups * sizeof(unsigned));
+  L.tickets = off; off = align_up(off + pik::kStepTickets * sizeof(unsigned));
   L.count = off; off = align_up(off + 2 * sizeof(int));
   L.src = off;   off = align_up(off + copies * sizeof(int));
   L.dst = off;   off = align_up(off + copies * sizeof(int));

@@ -63,22 +63,87 @@ __device__ __forceinline__ int wave_inclusive(int v) {
   return v;
 }
 
-// The codes of one block, as a wave loads them.
-template <int D> struct Codes {
-  u32x4 k[D / 32], v[D / 32];
-};
-
-template <int D>
-__device__ __forceinline__ void load_codes(Codes<D>& c, const uint8_t* k, const uint8_t* v) {
+// The codes of one block of K or V, as a wave loads them: 16 bytes a lane in each of D / 32 pieces.  A block
+// that is not there has 0 bytes: its loads read nothing and return 0, with no branch around them.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t codes_rsrc(const uint8_t* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00020000);
+}
+constexpr int kKvStream = 2;   // buffer cache policy nt: codes are read once
+__device__ __forceinline__ u32x4 codes_piece(__amdgpu_buffer_rsrc_t r, int piece) {
   const int lane = threadIdx.x & (WAVE - 1);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, 16 * lane + 1024 * piece, 0, kKvStream));
+}
+
+// Where the parts of a sequence and head lie that is spread over several workgroups, and what is joined there.
+// More than kFan parts are joined in two levels, by groups of about the square root of their number: one workgroup
+// joining 64 parts of 64 rows took 60 of 101 us.
+constexpr int kFan = 8;
+__device__ __forceinline__ int fan_of(int parts) { return parts <= kFan ? parts : (int)ceilf(sqrtf((float)parts)); }
+
+// The joined state of `n` parts (slots first, first + step, ... of the workspace; `start` is the slot whose
+// workgroup began the item) of R rows; sink(r, d, v, state) gets four dims of a row's O' and its state.
+template <int D, int kRows, class Sink>
+__device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* lds, int start, int from, int step, int n,
+                                           int R, Sink&& sink) {
+  constexpr int kRow = D + 4;
+  f32x4* state = reinterpret_cast<f32x4*>(lds);          // [n + 1][kRows]: the last is the joined one
+  auto word = [&](int i, int r) {
+    const int w = from + i * step;
+    return ((2 * w + (w == start ? 1 : 0)) * kRows + r) * kRow;
+  };
+  for (int k = threadIdx.x; k < n * kRows; k += blockDim.x) {
+    const int i = k / kRows, r = k % kRows;
+    if (r < R) state[k] = get4(prs, word(i, r) + D);
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < R) {
+    const int r = threadIdx.x;
+    RowState a{-INFINITY, -INFINITY, 0.0f};
+    for (int i = 0; i < n; ++i) {
+      a.rr = fmaxf(a.rr, state[i * kRows + r].x);
+      a.mm = fmaxf(a.mm, state[i * kRows + r].y);
+    }
+    for (int i = 0; i < n; ++i) {
+      const f32x4 b = state[i * kRows + r];
+      a.l += b.z * ex2_diff(b.y, a.mm);
+      state[i * kRows + r].x = ex2_diff(b.x, a.rr);
+    }
+    state[n * kRows + r] = f32x4{a.rr, a.mm, a.l, 0.f};
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < R * (D / 4); k += blockDim.x) {
+    const int r = k / (D / 4), d = 4 * (k % (D / 4));
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < n; i += kFan) {
+      f32x4 y[kFan];
 #pragma unroll
-  for (int q = 0; q < D / 32; ++q) c.k[q] = ld_stream(reinterpret_cast<const u32x4*>(k + q * 1024) + lane);
+      for (int e = 0; e < kFan; ++e) y[e] = get4(prs, word(min(i + e, n - 1), r) + d);
 #pragma unroll
-  for (int q = 0; q < D / 32; ++q) c.v[q] = ld_stream(reinterpret_cast<const u32x4*>(v + q * 1024) + lane);
+      for (int e = 0; e < kFan; ++e)
+        if (i + e < n) v += y[e] * state[(i + e) * kRows + r].x;
+    }
+    const f32x4 s = state[n * kRows + r];
+    sink(r, d, v, RowState{s.x, s.y, s.z});
+  }
+}
+
+// Counts this workgroup in; true in the last of `n`, which also clears the ticket.  The workgroup's partial
+// stores are complete in every wave before the ticket is drawn.
+__device__ __forceinline__ bool last_of(unsigned* ticket, int n, int* s_last) {
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool last =
+        __hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned)(n - 1);
+    if (last) __hip_atomic_store(ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *s_last = last;
+  }
+  __syncthreads();
+  return *s_last != 0;
 }
 
 template <int ACT, int CODE, int D, int NT>
-__global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k_kv_step(const KvAttendArgs A) {
+__global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_step(const KvAttendArgs A) {
   using T = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
   constexpr int kRows = 16 * NT, kRow = D + 4;        // rows of a tile; floats of a row's partial
@@ -174,103 +239,103 @@ __global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k
     const int count = b1 - b0 > wave ? (b1 - b0 - wave + kWaves - 1) / kWaves : 0;
     for (int k0 = 0; k0 < count; k0 += WAVE) {
       // where 64 of them lie: lane k holds block k0 + k
-      int page = -1, slot = 0, blk = 0, exps = 0;
-      const int m = min(count - k0, WAVE);
-      if (lane < m) {
-        const int bi = b0 + wave + (k0 + lane) * kWaves;
-        if (bi < span.count()) {
-          blk = span.block(bi);
-          page = kv_page(c, seq, blk);
-          slot = blk % c.page_blocks;
-        }
-        if (page >= 0) {
-          const size_t e = block_at(c, page, head, slot);
-          exps = (int)c.k_exp[e] | (int)c.v_exp[e] << 8;
-        }
-      }
-      Codes<D> cur, nxt;
-      auto fetch = [&](int k, Codes<D>& to) {
-        const size_t e = block_at(c, max(lane_of(page, k), 0), head, lane_of(slot, k)) * (kKvBlock * D);
-        load_codes<D>(to, c.k + e, c.v + e);
+      const int m = min(count - k0, WAVE), bi = b0 + wave + (k0 + lane) * kWaves;
+      const int blk = span.block(min(bi, max(span.count() - 1, 0)));
+      const int slot = blk % c.page_blocks, there = kv_page(c, max(seq, 0), blk);
+      const int page = lane < m && bi < span.count() ? there : -1;
+      const size_t eat = block_at(c, max(page, 0), head, slot);
+      const int exps = (int)c.k_exp[eat] | (int)c.v_exp[eat] << 8;
+      // the block after this one is on its way while this one is computed: a piece's registers are loaded
+      // again as soon as its codes are decoded
+      u32x4 kc[D / 32], vc[D / 32];
+      auto rsrc = [&](const uint8_t* base, int k) {
+        const int pg = lane_of(page, k & (WAVE - 1));
+        const size_t e = block_at(c, max(pg, 0), head, lane_of(slot, k & (WAVE - 1))) * (kKvBlock * D);
+        return codes_rsrc(base + e, k < m && pg >= 0 ? kKvBlock * D : 0);
       };
-      fetch(0, cur);
+      {
+        const __amdgpu_buffer_rsrc_t rk = rsrc(c.k, 0), rv = rsrc(c.v, 0);
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) kc[p] = codes_piece(rk, p);
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) vc[p] = codes_piece(rv, p);
+      }
       for (int k = 0; k < m; ++k) {
-        if (k + 1 < m) fetch(k + 1, nxt);
         const int t0 = lane_of(blk, k) * kKvBlock;
-        if (lane_of(page, k) >= 0) {
-          const int ex = lane_of(exps, k);
-          const int ek = max((ex & 255) - 127, -126), ev = max((ex >> 8) - 127, -126);
-          const float evf = (float)ev;
-          // scores: register 4 t + i of the lane is token t0 + 8 g + 4 t + i
-          float s[NT][8];
+        const bool held = lane_of(page, k) >= 0;
+        const __amdgpu_buffer_rsrc_t rk = rsrc(c.k, k + 1), rv = rsrc(c.v, k + 1);
+        const int ex = lane_of(exps, k);
+        const int ek = max((ex & 255) - 127, -126), ev = max((ex >> 8) - 127, -126);
+        const float evf = (float)ev;
+        // scores: register 4 t + i of the lane is token t0 + 8 g + 4 t + i
+        float s[NT][8];
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            f16x8 a[D / 32];
+        for (int t = 0; t < 2; ++t) {
+          f16x8 a[D / 32];
 #pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-              const u32x4 x = cur.k[t * (D / 64) + w];
-              a[2 * w] = decode8<CODE>(x.x, x.y);
-              a[2 * w + 1] = decode8<CODE>(x.z, x.w);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int w = 0; w < D / 32; ++w)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[w], q[n][w], acc, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[i];
-            }
+          for (int w = 0; w < D / 64; ++w) {
+            const int p = t * (D / 64) + w;
+            a[2 * w] = decode8<CODE>(kc[p].x, kc[p].y);
+            a[2 * w + 1] = decode8<CODE>(kc[p].z, kc[p].w);
+            kc[p] = codes_piece(rk, p);
           }
-          // every row sees the whole block unless it reaches past the first row or before a window
-          if (t0 + kKvBlock - 1 > p0 || (A.window > 0 && t0 <= p1 - A.window)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                s[n][j] = row_sees(pos[n], t0 + 8 * g + j, A.window, A.sinks) ? s[n][j] : -INFINITY;
-            // codes past the end are whatever the memory held
-            const int left = min(max(len - (t0 + 8 * g), 0), 8);
-            const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-            const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
-#pragma unroll
-            for (int p = 0; p < D / 32; ++p) cur.v[p] &= u32x4{lo, hi, lo, hi};
-          }
-          float mul[NT], top[NT];
-          bool move = false;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mul[n] = score_factor(row_mul[n], ek);
-            top[n] = s[n][0];
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int j = 1; j < 8; ++j) top[n] = fmaxf(top[n], s[n][j]);
-            top[n] *= mul[n];
-            move |= passes(st[n], top[n], evf);
-          }
-          if (__any(move)) {
+            for (int w = 0; w < D / 32; ++w) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[w], q[n][w], acc, 0, 0, 0);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float x = fmaxf(top[n], __shfl_xor(top[n], 16));
-              x = fmaxf(x, __shfl_xor(x, 32));
-              const float f = move_refs(st[n], x, evf);
-#pragma unroll
-              for (int d = 0; d < D / 16; ++d) o[n][d] *= f;
-            }
-          }
-          f16x8 w[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) weigh<8>(st[n], s[n], mul[n], evf, &w[n]);
-#pragma unroll
-          for (int p = 0; p < D / 32; ++p) {
-            const f16x8 a = decode8<CODE>(cur.v[p].x, cur.v[p].y), b = decode8<CODE>(cur.v[p].z, cur.v[p].w);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              o[n][2 * p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[n], o[n][2 * p], 0, 0, 0);
-              o[n][2 * p + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, w[n], o[n][2 * p + 1], 0, 0, 0);
-            }
+            for (int i = 0; i < 4; ++i) s[n][4 * t + i] = acc[i];
           }
         }
-        if (k + 1 < m) cur = nxt;
+        // every row sees the whole block unless it reaches past the first row or before a window
+        if (!held || t0 + kKvBlock - 1 > p0 || (A.window > 0 && t0 <= p1 - A.window)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              s[n][j] = held && row_sees(pos[n], t0 + 8 * g + j, A.window, A.sinks) ? s[n][j] : -INFINITY;
+          // codes past the end are whatever the memory held
+          const int left = min(max(len - (t0 + 8 * g), 0), 8);
+          const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+          const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
+#pragma unroll
+          for (int p = 0; p < D / 32; ++p) vc[p] &= u32x4{lo, hi, lo, hi};
+        }
+        float mul[NT], top[NT];
+        bool move = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mul[n] = score_factor(row_mul[n], ek);
+          top[n] = s[n][0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) top[n] = fmaxf(top[n], s[n][j]);
+          top[n] *= mul[n];
+          move |= passes(st[n], top[n], evf);
+        }
+        if (__any(move)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float x = fmaxf(top[n], __shfl_xor(top[n], 16));
+            x = fmaxf(x, __shfl_xor(x, 32));
+            const float f = move_refs(st[n], x, evf);
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) o[n][d] *= f;
+          }
+        }
+        f16x8 w[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) weigh<8>(st[n], s[n], mul[n], evf, &w[n]);
+#pragma unroll
+        for (int p = 0; p < D / 32; ++p) {
+          const f16x8 a = decode8<CODE>(vc[p].x, vc[p].y), b = decode8<CODE>(vc[p].z, vc[p].w);
+          vc[p] = codes_piece(rv, p);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            o[n][2 * p] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[n], o[n][2 * p], 0, 0, 0);
+            o[n][2 * p + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, w[n], o[n][2 * p + 1], 0, 0, 0);
+          }
+        }
       }
     }
 
@@ -288,7 +353,19 @@ __global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k
     __syncthreads();
     const bool whole = b0 == 0 && item + cost <= end;
     const int first = item / share, last = (item + cost - 1) / share;   // the workgroups it is spread over
-    const int part = 2 * (int)blockIdx.x + ((int)blockIdx.x == first ? 1 : 0);
+    auto store_row = [&](int r, int d, const f32x4& v, const RowState& a) {
+      const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
+      T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
+      const float half = out_half(a);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
+      if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
+    };
+    auto store_part = [&](int w, int r, int d, const f32x4& v, const RowState& a) {
+      const int to = ((2 * w + (w == first ? 1 : 0)) * kRows + r) * kRow;
+      put4(prs, to + d, v);
+      if (d == 0) put4(prs, to + D, f32x4{a.rr, a.mm, a.l, 0.f});
+    };
     for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
       const int r = k / (D / 4), d = 4 * (k % (D / 4));
       RowState a{-INFINITY, -INFINITY, 0.0f};
@@ -300,56 +377,27 @@ __global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k
         join(a, RowState{b.x, b.y, b.z}, fa, fb);
         v = v * fa + *reinterpret_cast<const f32x4*>(&s_part[w][r][d]) * fb;
       }
-      if (!whole) {
-        const int to = (part * kRows + r) * kRow;
-        put4(prs, to + d, v);
-        if (d == 0) put4(prs, to + D, f32x4{a.rr, a.mm, a.l, 0.f});
-        continue;
-      }
-      const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
-      T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
-      const float half = out_half(a);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
-      if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
+      if (whole)
+        store_row(r, d, v, a);
+      else
+        store_part(blockIdx.x, r, d, v, a);
     }
     if (!whole) {
-      // every wave's partial stores are complete before the barrier, the ticket is drawn after it
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (threadIdx.x == 0)
-        s_last = __hip_atomic_fetch_add(A.tickets + first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                 (unsigned)(last - first);
-      __syncthreads();
-      if (s_last) {
-        for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
-          const int r = k / (D / 4), d = 4 * (k % (D / 4));
-          RowState a{-INFINITY, -INFINITY, 0.0f};
-          f32x4 v = {0.f, 0.f, 0.f, 0.f};
-          for (int p = first; p <= last; p += 4) {
-            f32x4 x[4], y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int from = ((2 * min(p + e, last) + (p + e == first ? 1 : 0)) * kRows + r) * kRow;
-              x[e] = get4(prs, from + D);
-              y[e] = get4(prs, from + d);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (p + e <= last) {
-                float fa, fb;
-                join(a, RowState{x[e].x, x[e].y, x[e].z}, fa, fb);
-                v = v * fa + y[e] * fb;
-              }
-          }
-          const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
-          T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
-          const float half = out_half(a);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
-          if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
+      // parts that belong together: `fan` workgroups from w0, then all that lead such a group.  A group of one draws no
+      // ticket, so no two items share one: where one item ends in the workgroup where another begins, it ends alone.
+      const int parts = last - first + 1, fan = fan_of(parts), groups = (parts + fan - 1) / fan;
+      const int w0 = first + ((int)blockIdx.x - first) / fan * fan, n = min(fan, last + 1 - w0);
+      if (n == 1 || last_of(A.tickets + w0, n, &s_last)) {
+        float* lds = &s_part[0][0][0];
+        if (groups == 1) {
+          join_parts<D, kRows>(prs, lds, first, first, 1, n, R, store_row);
+        } else {
+          if (n > 1)
+            join_parts<D, kRows>(prs, lds, first, w0, 1, n, R,
+                                 [&](int r, int d, const f32x4& v, const RowState& a) { store_part(w0, r, d, v, a); });
+          if (last_of(A.tickets + kStepTickets / 2 + first, groups, &s_last))
+            join_parts<D, kRows>(prs, lds, first, first, fan, groups, R, store_row);
         }
-        if (threadIdx.x == 0) __hip_atomic_store(A.tickets + first, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
     __syncthreads();   // s_part is free again
@@ -359,7 +407,7 @@ __global__ __launch_bounds__(WAVE* kWaves, (NT == 4 && D == 128) ? 1 : 2) void k
 
 template <int ACT, int CODE, int D, int NT>
 hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(kStepGroups), dim3(WAVE * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(step_groups(NT, D)), dim3(WAVE * kWaves), 0, s, a);
   return hipGetLastError();
 }
 
