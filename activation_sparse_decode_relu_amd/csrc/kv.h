@@ -57,11 +57,13 @@ constexpr int kStepRows = 64, kStepGrain = 8;
 constexpr int step_groups(int tiles, int dim) {
   return 256 * (tiles == 1 ? (dim == 64 ? 4 : 3) : tiles == 4 && dim == 128 ? 1 : 2);
 }
-constexpr int kStepTickets = 2 * 1024;
-// a workgroup leaves two parts at most: of the item it starts in and of the one it ends in
+// Pieces a call's items (sequences times cached heads) are cut into at most, and workgroups it is launched with
+// at most.  Those of items that are cut leave a part each: at most 2 * step_groups.
+constexpr int step_pieces(int groups, int items) { return items + groups / 2 > groups ? items + groups / 2 : groups; }
+constexpr int kStepLaunch = 4096, kStepTickets = 2 * 2048;
 constexpr size_t step_partial_floats(int dim) { return (size_t)2 * 512 * kStepRows * (dim + 4); }
 static_assert(step_groups(1, 64) * 16 <= 512 * kStepRows && step_groups(1, 128) * 16 <= 512 * kStepRows &&
-              step_groups(2, 64) * 32 <= 512 * kStepRows && step_groups(1, 64) <= kStepTickets / 2, "workspace");
+              step_groups(2, 64) * 32 <= 512 * kStepRows && step_groups(1, 64) <= kStepTickets / 4, "workspace");
 hipError_t launch_kv_step(int act, int code, const KvAttendArgs& a, hipStream_t s);
 // Any number of rows, kTileRows a workgroup; where that leaves fewer than kTileParts / 2 workgroups, the
 // tokens of each are split over up to kTileParts in all.

@@ -26,10 +26,16 @@ __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x)
 // 2^(a - b) where a <= b and a may be -inf (then 0, whatever b is).
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == -INFINITY ? 0.0f : ex2(a - b); }
 
-// One row's running state: references, and this lane's part of the sum.
+// One row's state: references, and (this lane's part of) the sum.
 struct RowState {
   float rr, mm, l;
 };
+
+// The same while blocks come in, with what weigh() takes of the references worked out when they move.
+struct RowRun : RowState {
+  float c, g;   // rr - kBias and rr - kBias - mm; 0 and -inf before the first score
+};
+__device__ __forceinline__ RowRun row_run() { return RowRun{{-INFINITY, -INFINITY, 0.0f}, 0.0f, -INFINITY}; }
 
 // The factor of a block's scores, in the range in which no infinity or zero comes from it alone.
 __device__ __forceinline__ float score_factor(float row, int ek) {
@@ -43,21 +49,21 @@ __device__ __forceinline__ bool passes(const RowState& s, float top, float ev) {
 
 // New references from the row's largest score of the block (the same in all of the row's lanes);
 // returns what O' has to be multiplied with.
-__device__ __forceinline__ float move_refs(RowState& s, float top, float ev) {
+__device__ __forceinline__ float move_refs(RowRun& s, float top, float ev) {
   const float rr = fmaxf(s.rr, top + ev), mm = fmaxf(s.mm, top);
   const float f = ex2_diff(s.rr, rr);
   s.l *= ex2_diff(s.mm, mm);
   s.rr = rr;
   s.mm = mm;
+  s.c = rr > -INFINITY ? rr - kBias : 0.0f;
+  s.g = rr > -INFINITY ? rr - kBias - mm : -INFINITY;
   return f;
 }
 
 // Scores s[N] of one block (raw sums; -inf where masked) -> fp16 weights, N = 8 or 16, and the row's sum.
 template <int N>
-__device__ __forceinline__ void weigh(RowState& st, const float* s, float mul, float ev, f16x8* w) {
-  const bool any = st.rr > -INFINITY;
-  const float e = fmaxf(ev, st.rr - st.mm - kFar);       // -inf minus -inf is NaN: ev
-  const float d = any ? e - st.rr + kBias : 0.0f;
+__device__ __forceinline__ void weigh(RowRun& st, const float* s, float mul, float ev, f16x8* w) {
+  const float e = fmaxf(ev, st.g - (kFar - kBias)), d = e - st.c;
   float sum = 0.0f;
 #pragma unroll
   for (int q = 0; q < N / 8; ++q) {
@@ -67,7 +73,7 @@ __device__ __forceinline__ void weigh(RowState& st, const float* s, float mul, f
     sum += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     w[q] = f16x8{(f16)p[0], (f16)p[1], (f16)p[2], (f16)p[3], (f16)p[4], (f16)p[5], (f16)p[6], (f16)p[7]};
   }
-  st.l = any ? fmaf(sum, ex2(st.rr - kBias - e - st.mm), st.l) : st.l;
+  st.l = fmaf(sum, ex2(st.g - e), st.l);
 }
 
 // O' -> out: 2^(rr - kBias - mm) can be far below what exp2 returns, so it is applied in two halves.

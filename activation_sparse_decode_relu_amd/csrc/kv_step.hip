@@ -1,16 +1,26 @@
 // Attention of few rows: single tokens and a handful (up to 64 rows of a cached head), over long caches.
 //
-// Bound by reading the codes, so the split is over bytes.  The call's blocks of 32 tokens, over all
-// sequences and cached heads, stand in one line; each of a fixed number of workgroups takes an equal
-// stretch of it, whatever the lengths are, and works out its stretch itself from the lengths (they
-// are on the device).  The four waves of a workgroup take the blocks of a stretch in turn, each with its
-// own online softmax, straight from memory to the matrix instructions' operands: a block's bytes are stored
-// in their order, so each load is one contiguous KB and nothing passes through LDS.  One
-// 16x16x32 tile holds up to 16 rows: all query heads of a cached head, for all its new tokens.
+// Bound by reading the codes.  An item is a sequence and cached head with its blocks of 32 tokens; items are cut
+// into pieces of up to S blocks, one workgroup each, so that the card is filled once: S is the smallest of five
+// sizes from (blocks of the call) / (workgroups the card holds) to twice that which gives no more pieces than
+// fit, or, with many items, half a round more than there are items.  Every workgroup works this out by itself
+// from the lengths (they are on the device).  Starting a piece costs as much as some 8 blocks (its lengths, pages
+// and codes are loads that wait for each other), so whole items are better than equal stretches of the call's
+// blocks: 64 sequences of 1000 tokens, 8 heads, took 36.4 us with equal stretches and take 27.3.
 //
-// A sequence and head that lies in one stretch is finished by its workgroup; otherwise each workgroup leaves
-// its state (fp32) in the workspace and the last of them, by a ticket, joins the parts in their order,
-// so the result does not depend on who was last.
+// The four waves of a workgroup take the blocks of a piece in turn, each with its own online softmax,
+// straight from memory to the matrix instructions' operands: a block's bytes are stored in their order, so
+// each load is one contiguous KB and nothing passes through LDS.  One 16x16x32 tile holds up to 16 rows:
+// all query heads of a cached head, for all its new tokens.
+//
+// An item of one piece is finished by its workgroup; otherwise each workgroup leaves its state (fp32) in the
+// workspace and the last of them, by a ticket, joins the parts in their order, so the result does not depend
+// on who was last.
+//
+// Measured: long caches stream at 6.0 TB/s (64 x 4000 tokens, 526 MB in 87.7 us) and some 9 us go to the start
+// and the end, in which nothing streams.
+#include <algorithm>
+
 #include "kv_softmax.h"
 
 namespace pik {
@@ -19,18 +29,15 @@ namespace {
 
 constexpr int kWaves = 4;
 
-// What one sequence brings to the line, as a lane holds it.
+// What one sequence brings to the call, as a lane holds it.
 struct StepSeq {
   int seq, len, row0, rows;   // rows: those computed, at most max_new
   int p0;                     // position of its first row
-  int blocks;                 // visible blocks, at least 1
-  int units;                  // places in the line: kv_heads * (blocks rounded up to kStepGrain)
+  int blocks;                 // visible blocks, at least 1 where there are rows
 };
 
-__device__ __forceinline__ int grain_up(int blocks) { return (blocks + kStepGrain - 1) / kStepGrain * kStepGrain; }
-
 __device__ __forceinline__ StepSeq step_seq(const KvAttendArgs& A, int i) {
-  StepSeq r{-1, 0, 0, 0, 0, 1, 0};
+  StepSeq r{-1, 0, 0, 0, 0, 0};
   if (i >= A.c.n) return r;
   const KvSeq s = kv_seq(A.c, i);
   r.seq = s.seq;
@@ -38,30 +45,26 @@ __device__ __forceinline__ StepSeq step_seq(const KvAttendArgs& A, int i) {
   r.row0 = s.row0;
   r.rows = min(s.rows, A.max_new);
   r.p0 = s.len - s.rows;
-  if (r.rows > 0) {
-    r.blocks = max(span_of(r.p0, r.p0 + r.rows - 1, A.window, A.sinks).count(), 1);
-    r.units = grain_up(r.blocks) * A.c.kv_heads;
-  }
+  if (r.rows > 0) r.blocks = max(span_of(r.p0, r.p0 + r.rows - 1, A.window, A.sinks).count(), 1);
   return r;
 }
 
 __device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-__device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int m = 1; m < WAVE; m <<= 1) v += __shfl_xor(v, m);
-  return __builtin_amdgcn_readfirstlane(v);
-}
-
+// Inclusive sums over the wave's lanes, and all of them (both of the vector ALU alone).
 __device__ __forceinline__ int wave_inclusive(int v) {
-  const int lane = threadIdx.x & (WAVE - 1);
-#pragma unroll
-  for (int off = 1; off < WAVE; off <<= 1) {
-    const int y = __shfl_up(v, off, WAVE);
-    if (lane >= off) v += y;
-  }
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);   // row_shr 1, 2, 4, 8: within 16 lanes
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15: rows 1 and 3 take the row before
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31: the upper half takes the lower
   return v;
 }
+__device__ __forceinline__ int wave_total(int v) { return lane_of(wave_inclusive(v), WAVE - 1); }
+
+// Into how many pieces of about S blocks an item of `blocks` falls.
+__device__ __forceinline__ int pieces_of(int blocks, int S) { return (int)((unsigned)(blocks + S - 1) / (unsigned)S); }
 
 // The codes of one block of K or V, as a wave loads them: 16 bytes a lane in each of D / 32 pieces.  A block
 // that is not there has 0 bytes: its loads read nothing and return 0, with no branch around them.
@@ -80,18 +83,26 @@ __device__ __forceinline__ u32x4 codes_piece(__amdgpu_buffer_rsrc_t r, int piece
 constexpr int kFan = 8;
 __device__ __forceinline__ int fan_of(int parts) { return parts <= kFan ? parts : (int)ceilf(sqrtf((float)parts)); }
 
-// The joined state of `n` parts (slots first, first + step, ... of the workspace; `start` is the slot whose
-// workgroup began the item) of R rows; sink(r, d, v, state) gets four dims of a row's O' and its state.
+// The joined state of `n` parts (slots from, from + step, ... of the workspace) of R rows; sink(r, d, v, state) gets four dims of a row's O' and its state.
 template <int D, int kRows, class Sink>
-__device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* lds, int start, int from, int step, int n,
-                                           int R, Sink&& sink) {
+__device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* lds, int from, int step, int n, int R,
+                                           Sink&& sink) {
   constexpr int kRow = D + 4;
   f32x4* state = reinterpret_cast<f32x4*>(lds);          // [n + 1][kRows]: the last is the joined one
-  auto word = [&](int i, int r) {
-    const int w = from + i * step;
-    return ((2 * w + (w == start ? 1 : 0)) * kRows + r) * kRow;
+  auto word = [&](int i, int r) { return ((from + i * step) * kRows + r) * kRow; };
+  // every load of a batch of parts is on its way before the first is used, the first batch before the states
+  constexpr int kThreads = WAVE * kWaves, kMine = kRows * (D / 4) / kThreads, kBatch = 16 / kMine;
+  f32x4 y[kMine][kBatch], v[kMine];
+  auto batch = [&](int i0) {
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+      const int k = q * kThreads + threadIdx.x, r = min(k / (D / 4), R - 1), d = 4 * (k % (D / 4));
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) y[q][e] = get4(prs, word(min(i0 + e, n - 1), r) + d);
+    }
   };
-  for (int k = threadIdx.x; k < n * kRows; k += blockDim.x) {
+  batch(0);
+  for (int k = threadIdx.x; k < n * kRows; k += kThreads) {
     const int i = k / kRows, r = k % kRows;
     if (r < R) state[k] = get4(prs, word(i, r) + D);
   }
@@ -111,19 +122,24 @@ __device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* ld
     state[n * kRows + r] = f32x4{a.rr, a.mm, a.l, 0.f};
   }
   __syncthreads();
-  for (int k = threadIdx.x; k < R * (D / 4); k += blockDim.x) {
-    const int r = k / (D / 4), d = 4 * (k % (D / 4));
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < n; i += kFan) {
-      f32x4 y[kFan];
 #pragma unroll
-      for (int e = 0; e < kFan; ++e) y[e] = get4(prs, word(min(i + e, n - 1), r) + d);
+  for (int q = 0; q < kMine; ++q) v[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    if (i0 > 0) batch(i0);
 #pragma unroll
-      for (int e = 0; e < kFan; ++e)
-        if (i + e < n) v += y[e] * state[(i + e) * kRows + r].x;
+    for (int q = 0; q < kMine; ++q) {
+      const int r = min((int)(q * kThreads + threadIdx.x) / (D / 4), R - 1);
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (i0 + e < n) v[q] += y[q][e] * state[(i0 + e) * kRows + r].x;
     }
+  }
+#pragma unroll
+  for (int q = 0; q < kMine; ++q) {
+    const int k = q * kThreads + threadIdx.x, r = k / (D / 4), d = 4 * (k % (D / 4));
+    if (r >= R) continue;
     const f32x4 s = state[n * kRows + r];
-    sink(r, d, v, RowState{s.x, s.y, s.z});
+    sink(r, d, v[q], RowState{s.x, s.y, s.z});
   }
 }
 
@@ -154,45 +170,53 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
   const int g = lane >> 4, col = lane & 15;
   const __amdgpu_buffer_rsrc_t prs = partial_rsrc(A.partial);
 
-  // ---- this workgroup's stretch of the line --------------------------------------------------------
+  // ---- the pieces: see the top of the file --------------------------------------------------------
+  constexpr int G = step_groups(NT, D), kTries = 5;
   StepSeq mine = step_seq(A, lane);
-  int total = mine.units;
-  for (int base = WAVE; base < c.n; base += WAVE) total += step_seq(A, base + lane).units;
-  total = wave_total(total);
-  // equal shares, in whole grains
-  const int share = grain_up((int)(((long long)total + gridDim.x - 1) / gridDim.x));
-  const int begin = (int)min((long long)blockIdx.x * share, (long long)total);
-  const int end = min(begin + share, total);
-  if (begin >= end) return;
-  int base = 0, before = 0;                           // the 64 sequences in `mine`, and the units before them
-  int incl = wave_inclusive(mine.units);
-  while (before + lane_of(incl, WAVE - 1) <= begin) {
-    before += lane_of(incl, WAVE - 1);
-    base += WAVE;
-    mine = step_seq(A, base + lane);
-    incl = wave_inclusive(mine.units);
+  int sum = mine.blocks;
+  for (int base = WAVE; base < c.n; base += WAVE) sum += step_seq(A, base + lane).blocks;
+  const int total = wave_total(sum) * c.kv_heads;
+  int S = 0;
+  {
+    int tries[kTries], got[kTries];
+#pragma unroll
+    for (int e = 0; e < kTries; ++e) {
+      tries[e] = max((int)(((long long)total * (4 + e) + 4 * G - 1) / (4 * G)), kStepGrain);
+      got[e] = pieces_of(mine.blocks, tries[e]);
+    }
+    for (int base = WAVE; base < c.n; base += WAVE) {
+      const int blocks = step_seq(A, base + lane).blocks;
+#pragma unroll
+      for (int e = 0; e < kTries; ++e) got[e] += pieces_of(blocks, tries[e]);
+    }
+    const int most = step_pieces(G, c.n * c.kv_heads);
+#pragma unroll
+    for (int e = kTries - 1; e >= 0; --e)
+      if (e == kTries - 1 || wave_total(got[e]) * c.kv_heads <= most) S = tries[e];
   }
-  int at = __builtin_ctzll(__ballot(before + incl > begin));   // lane of the sequence that holds `begin`
+  int base = 0, before = 0, slots = 0;                // the 64 sequences in `mine`, the pieces and slots before them
+  int pieces = pieces_of(mine.blocks, S);
+  int incl = wave_inclusive(pieces) * c.kv_heads;
+  int incl_slots = wave_inclusive(pieces > 1 ? pieces : 0) * c.kv_heads;
 
-  for (int u = begin; u < end;) {
-    if (at == WAVE || before + lane_of(incl, WAVE - 1) <= u) {
+  for (int w = blockIdx.x;; w += gridDim.x) {
+    while (before + lane_of(incl, WAVE - 1) <= w) {
       before += lane_of(incl, WAVE - 1);
+      slots += lane_of(incl_slots, WAVE - 1);
       base += WAVE;
+      if (base >= c.n) return;
       mine = step_seq(A, base + lane);
-      incl = wave_inclusive(mine.units);
-      at = __builtin_ctzll(__ballot(before + incl > u));
+      pieces = pieces_of(mine.blocks, S);
+      incl = wave_inclusive(pieces) * c.kv_heads;
+      incl_slots = wave_inclusive(pieces > 1 ? pieces : 0) * c.kv_heads;
     }
+    const int at = __builtin_ctzll(__ballot(before + incl > w));   // lane of the piece's sequence
     const int seq = lane_of(mine.seq, at), len = lane_of(mine.len, at), row0 = lane_of(mine.row0, at);
-    const int nrows = lane_of(mine.rows, at), p0 = lane_of(mine.p0, at), units = lane_of(mine.units, at);
-    const int blocks = lane_of(mine.blocks, at), first_unit = before + lane_of(incl, at) - units;
-    if (units == 0 || u >= first_unit + units) {
-      ++at;
-      continue;
-    }
-    const int cost = grain_up(blocks), head = (u - first_unit) / cost;
-    const int item = first_unit + head * cost;        // where this sequence and head begins in the line
-    const int b0 = u - item, b1 = min(min(cost, b0 + end - u), blocks);
-    const int next = min(item + cost, end);
+    const int nrows = lane_of(mine.rows, at), p0 = lane_of(mine.p0, at), blocks = lane_of(mine.blocks, at);
+    const int parts = lane_of(pieces, at), local = w - (before + lane_of(incl, at) - parts * c.kv_heads);
+    const int head = local / parts, part = local - head * parts;
+    const int first = slots + lane_of(incl_slots, at) - (c.kv_heads - head) * parts;   // slot of part 0, if parts > 1
+    const int per = (blocks + parts - 1) / parts, b0 = part * per, b1 = min(b0 + per, blocks);
     const int p1 = p0 + nrows - 1, R = nrows * A.group;
     Span span = span_of(p0, p1, A.window, A.sinks);
     if (seq < 0) span = Span{0, 0, 0};
@@ -202,7 +226,7 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
     f16x8 q[NT][D / 32];
     float row_mul[NT];
     int pos[NT];
-    RowState st[NT];
+    RowRun st[NT];
     f32x4 o[NT][D / 16];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -230,7 +254,7 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
 #pragma unroll
       for (int s = 0; s < D / 32; ++s) q[t][s] = query8<ACT>(x[s], up);
       row_mul[t] = A.scale * kLog2e * down;
-      st[t] = RowState{-INFINITY, -INFINITY, 0.0f};
+      st[t] = row_run();
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) o[t][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -351,63 +375,75 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
       if (g == 0) *reinterpret_cast<f32x4*>(to + D) = f32x4{st[n].rr, st[n].mm, l, 0.f};
     }
     __syncthreads();
-    const bool whole = b0 == 0 && item + cost <= end;
-    const int first = item / share, last = (item + cost - 1) / share;   // the workgroups it is spread over
     auto store_row = [&](int r, int d, const f32x4& v, const RowState& a) {
       const int j = (r * inv_group) >> 16, h = head * A.group + r - j * A.group;
       T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
       const float half = out_half(a);
+      typedef T T4 __attribute__((ext_vector_type(4)));
+      T4 y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) out[e] = (T)out_value(v[e], a.l, half);
+      for (int e = 0; e < 4; ++e) y[e] = (T)out_value(v[e], a.l, half);
+      *reinterpret_cast<T4*>(out) = y;
       if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
     };
-    auto store_part = [&](int w, int r, int d, const f32x4& v, const RowState& a) {
-      const int to = ((2 * w + (w == first ? 1 : 0)) * kRows + r) * kRow;
+    auto store_part = [&](int at, int r, int d, const f32x4& v, const RowState& a) {
+      const int to = (at * kRows + r) * kRow;
       put4(prs, to + d, v);
       if (d == 0) put4(prs, to + D, f32x4{a.rr, a.mm, a.l, 0.f});
     };
-    for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
-      const int r = k / (D / 4), d = 4 * (k % (D / 4));
+    // the rows' joined states and the waves' factors, once a row
+    if ((int)threadIdx.x < R) {
       RowState a{-INFINITY, -INFINITY, 0.0f};
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      f32x4 x[kWaves];
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const f32x4 b = *reinterpret_cast<const f32x4*>(&s_part[w][r][D]);
-        float fa, fb;
-        join(a, RowState{b.x, b.y, b.z}, fa, fb);
-        v = v * fa + *reinterpret_cast<const f32x4*>(&s_part[w][r][d]) * fb;
+        x[w] = *reinterpret_cast<const f32x4*>(&s_part[w][threadIdx.x][D]);
+        a.rr = fmaxf(a.rr, x[w].x);
+        a.mm = fmaxf(a.mm, x[w].y);
       }
-      if (whole)
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        a.l += x[w].z * ex2_diff(x[w].y, a.mm);
+        s_part[w][threadIdx.x][D + 3] = ex2_diff(x[w].x, a.rr);
+      }
+      *reinterpret_cast<f32x4*>(&s_part[0][threadIdx.x][D]) = f32x4{a.rr, a.mm, a.l, s_part[0][threadIdx.x][D + 3]};
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < R * (D / 4); k += WAVE * kWaves) {
+      const int r = k / (D / 4), d = 4 * (k % (D / 4));
+      const f32x4 x = *reinterpret_cast<const f32x4*>(&s_part[0][r][D]);
+      f32x4 v = *reinterpret_cast<const f32x4*>(&s_part[0][r][d]) * x.w;
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_part[w][r][d]) * s_part[w][r][D + 3];
+      const RowState a{x.x, x.y, x.z};
+      if (parts == 1)
         store_row(r, d, v, a);
       else
-        store_part(blockIdx.x, r, d, v, a);
+        store_part(first + part, r, d, v, a);
     }
-    if (!whole) {
-      // parts that belong together: `fan` workgroups from w0, then all that lead such a group.  A group of one draws no
-      // ticket, so no two items share one: where one item ends in the workgroup where another begins, it ends alone.
-      const int parts = last - first + 1, fan = fan_of(parts), groups = (parts + fan - 1) / fan;
-      const int w0 = first + ((int)blockIdx.x - first) / fan * fan, n = min(fan, last + 1 - w0);
-      if (n == 1 || last_of(A.tickets + w0, n, &s_last)) {
+    if (parts > 1) {
+      // `fan` parts from w0 on are joined by the last of them, then these by the last of those
+      const int fan = fan_of(parts), groups = (parts + fan - 1) / fan;
+      const int w0 = first + part / fan * fan, m = min(fan, first + parts - w0);
+      if (last_of(A.tickets + w0, m, &s_last)) {
         float* lds = &s_part[0][0][0];
         if (groups == 1) {
-          join_parts<D, kRows>(prs, lds, first, first, 1, n, R, store_row);
+          join_parts<D, kRows>(prs, lds, first, 1, m, R, store_row);
         } else {
-          if (n > 1)
-            join_parts<D, kRows>(prs, lds, first, w0, 1, n, R,
-                                 [&](int r, int d, const f32x4& v, const RowState& a) { store_part(w0, r, d, v, a); });
+          join_parts<D, kRows>(prs, lds, w0, 1, m, R,
+                               [&](int r, int d, const f32x4& v, const RowState& a) { store_part(w0, r, d, v, a); });
           if (last_of(A.tickets + kStepTickets / 2 + first, groups, &s_last))
-            join_parts<D, kRows>(prs, lds, first, first, fan, groups, R, store_row);
+            join_parts<D, kRows>(prs, lds, first, fan, groups, R, store_row);
         }
       }
     }
     __syncthreads();   // s_part is free again
-    u = next;
   }
 }
 
 template <int ACT, int CODE, int D, int NT>
 hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(step_groups(NT, D)), dim3(WAVE * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(step_groups(NT, D), a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * kWaves), 0, s, a);
   return hipGetLastError();
 }
 

@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     for (int s = 0; s < D / 16; ++s) q[s] = query8<ACT>(x[s], up);
     row_mul = A.scale * kLog2e * down;
   }
-  RowState st{-INFINITY, -INFINITY, 0.0f};
+  RowRun st = row_run();
   f32x16 o[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
