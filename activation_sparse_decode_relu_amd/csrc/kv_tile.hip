@@ -53,10 +53,9 @@ __device__ __forceinline__ bool tile_job(const KvAttendArgs& A, int slot, int sp
   return split < j.splits;
 }
 
-// Two blocks on their way: where they are, and this thread's pieces of their codes.
-struct TileMeta {
-  int t0[2], exps[2];
-  bool held[2];
+// The two blocks of a tile: first token and exponents (K's, V's << 8), the latter -1 where there is no page.
+struct Tile {
+  int ta, tb, xa, xb;
 };
 
 template <int ACT, int CODE, int D>
@@ -112,7 +111,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
   // ---- tiles: memory -> registers -> LDS -----------------------------------------------------------------
   int vpage = -1, vslot = 0, vblk = 0, vexps = 0, window0 = 0, window1 = 0;   // lane k: block window0 + k of the span
   u32x4 codes[kMine];
-  auto fetch = [&](int tile, TileMeta& m) {
+  auto fetch = [&](int tile) {
     if (2 * tile >= window1) {
       window0 = 2 * tile;
       window1 = window0 + WAVE;
@@ -129,106 +128,112 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
         }
       }
     }
-    size_t at[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int k = 2 * tile - window0 + b;
-      const int page = __builtin_amdgcn_readlane(vpage, k);
-      m.held[b] = page >= 0;
-      m.t0[b] = __builtin_amdgcn_readlane(vblk, k) * kKvBlock;
-      m.exps[b] = __builtin_amdgcn_readlane(vexps, k);
-      at[b] = block_at(c, max(page, 0), head, __builtin_amdgcn_readlane(vslot, k)) * (kKvBlock * D);
-    }
+    const int k = 2 * tile - window0;
+    const int pa = __builtin_amdgcn_readlane(vpage, k), pb = __builtin_amdgcn_readlane(vpage, k + 1);
+    const size_t ea = block_at(c, max(pa, 0), head, __builtin_amdgcn_readlane(vslot, k)) * (kKvBlock * D);
+    const size_t eb = block_at(c, max(pb, 0), head, __builtin_amdgcn_readlane(vslot, k + 1)) * (kKvBlock * D);
 #pragma unroll
     for (int e = 0; e < kMine; ++e) {
       const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
-      const uint8_t* p = (sec < 2 ? c.k : c.v) + at[sec & 1];
+      const uint8_t* p = (sec < 2 ? c.k : c.v) + ((sec & 1) ? eb : ea);
       codes[e] = *(reinterpret_cast<const u32x4*>(p) + w);
     }
+    return Tile{__builtin_amdgcn_readlane(vblk, k) * kKvBlock, __builtin_amdgcn_readlane(vblk, k + 1) * kKvBlock,
+                pa < 0 ? -1 : __builtin_amdgcn_readlane(vexps, k), pb < 0 ? -1 : __builtin_amdgcn_readlane(vexps, k + 1)};
   };
-  auto stage = [&](int buf, const TileMeta& m) {
+  // this thread's pieces, decoded, to their places
+  auto stage = [&](int buf, const Tile& m) {
+    // V's codes of tokens that are not there may be anything, and their weight of 0 is not enough
+    if (m.xa < 0 || m.xb < 0 || max(m.ta, m.tb) + kKvBlock > job.s.len) {
+#pragma unroll
+      for (int e = 0; e < kMine; ++e) {
+        const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
+        if (sec < 2) continue;
+        const int t0 = (sec & 1) ? m.tb : m.ta, ex = (sec & 1) ? m.xb : m.xa;
+        const int left = ex < 0 ? 0 : min(max(job.s.len - (t0 + 8 * ((w / 16) % 4)), 0), 8);
+        const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+        const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
+        codes[e] &= u32x4{lo, hi, lo, hi};
+      }
+    }
 #pragma unroll
     for (int e = 0; e < kMine; ++e) {
       const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
-      const int b = sec & 1;
-      u32x4 x = codes[e];
-      if (sec < 2) {
-        const int t = w / D, chunk = (w / 16) % (D / 16), rr = w % 16;
-        const int row = 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);   // where the token's scores shall come out
-        s_k[buf][b][(2 * chunk) * 32 + row] = decode8<CODE>(x.x, x.y);
-        s_k[buf][b][(2 * chunk + 1) * 32 + row] = decode8<CODE>(x.z, x.w);
-      } else {
-        const int p = w / 64, g = (w / 16) % 4, dl = w % 16;
-        if (m.t0[b] + kKvBlock > job.s.len) {   // codes past the end are whatever the memory held
-          const int left = min(max(job.s.len - (m.t0[b] + 8 * g), 0), 8);
-          const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-          const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
-          x &= u32x4{lo, hi, lo, hi};
-        }
-        f16x8* to = &s_v[buf][b][((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + dl];
-        to[0] = decode8<CODE>(x.x, x.y);
-        to[16] = decode8<CODE>(x.z, x.w);
-      }
+      const int t = w / D, chunk = (w / 16) % (D / 16), rr = w % 16;
+      const int row = 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);   // where the token's scores shall come out
+      const int p = w / 64, g = (w / 16) % 4, dl = w % 16;
+      f16x8* to = sec < 2 ? &s_k[buf][sec & 1][2 * chunk * 32 + row]
+                          : &s_v[buf][sec & 1][((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + dl];
+      to[0] = decode8<CODE>(codes[e].x, codes[e].y);
+      to[sec < 2 ? 32 : 16] = decode8<CODE>(codes[e].z, codes[e].w);
     }
   };
-  auto compute = [&](int buf, const TileMeta& m) {
-    float s[2][16], mul[2], ev[2], top[2];
-    bool on[2], move = false;
+  // scores of a block: register e of the lane is token t0 + 16 (e / 8) + 8 h + e % 8
+  auto scores = [&](const f16x8* k) {
+    f32x16 acc;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int t0 = m.t0[b];
-      on[b] = m.held[b] && t0 <= wp1 &&
-              (A.window == 0 || t0 < A.sinks || t0 + kKvBlock - 1 > wp0 - A.window);
-      if (!on[b]) continue;
-      f32x16 acc;
+    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+    for (int s = 0; s < D / 16; ++s) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[64 * s + lane], q[s], acc, 0, 0, 0);
+    return acc;
+  };
+  auto mask = [&](f32x16& s, int t0, int ex) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(s_k[buf][b][64 * k + lane], q[k], acc, 0, 0, 0);
-      // register e of the lane is token t0 + 16 (e / 8) + 8 h + e % 8
+    for (int e = 0; e < 16; ++e)
+      s[e] = ex >= 0 && row_sees(pos, t0 + 16 * (e / 8) + 8 * h + e % 8, A.window, A.sinks) ? s[e] : -INFINITY;
+  };
+  auto top_of = [&](const f32x16& s) {
+    float m = s[0];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[b][e] = acc[e];
-      if (t0 + kKvBlock - 1 > wp0 || (A.window > 0 && t0 <= wp1 - A.window)) {
+    for (int e = 1; e < 16; ++e) m = fmaxf(m, s[e]);
+    return m;
+  };
+  auto values = [&](const f16x8* v, const f32x16& s, float mul, float ev) {
+    float x[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          s[b][e] = row_sees(pos, t0 + 16 * (e / 8) + 8 * h + e % 8, A.window, A.sinks) ? s[b][e] : -INFINITY;
-      }
-      mul[b] = score_factor(row_mul, max((m.exps[b] & 255) - 127, -126));
-      ev[b] = (float)max((m.exps[b] >> 8) - 127, -126);
-      top[b] = s[b][0];
+    for (int e = 0; e < 16; ++e) x[e] = s[e];
+    f16x8 w[2];
+    weigh<16>(st, x, mul, ev, w);
 #pragma unroll
-      for (int e = 1; e < 16; ++e) top[b] = fmaxf(top[b], s[b][e]);
-      top[b] *= mul[b];
-      move |= passes(st, top[b], ev[b]);
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[64 * (k * (D / 32) + d) + lane], w[k], o[d], 0, 0, 0);
+  };
+  auto move = [&](float top, float ev) {
+    const float f = move_refs(st, fmaxf(top, __shfl_xor(top, 32)), ev);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) o[d] *= f;
+  };
+  // does a row of this wave see the block; do all of them see all of it
+  auto seen = [&](int t0, int ex) {
+    return ex >= 0 && t0 <= wp1 && (A.window == 0 || t0 < A.sinks || t0 + kKvBlock - 1 > wp0 - A.window);
+  };
+  auto whole = [&](int t0, int ex) {
+    return ex >= 0 && t0 + kKvBlock - 1 <= wp0 && (A.window == 0 || t0 > wp1 - A.window);
+  };
+  auto compute = [&](int buf, const Tile& m) {
+    const float ka = score_factor(row_mul, max((m.xa & 255) - 127, -126)), kb = score_factor(row_mul, max((m.xb & 255) - 127, -126));
+    const float va = (float)max(((m.xa >> 8) & 255) - 127, -126), vb = (float)max(((m.xb >> 8) & 255) - 127, -126);
+    if (!seen(m.ta, m.xa) && !seen(m.tb, m.xb)) return;
+    f32x16 sa = scores(s_k[buf][0]), sb = scores(s_k[buf][1]);
+    if (!whole(m.ta, m.xa) || !whole(m.tb, m.xb)) {
+      mask(sa, m.ta, m.xa);
+      mask(sb, m.tb, m.xb);
     }
-    if (!on[0] && !on[1]) return;
-    if (__any(move)) {
-      float f = 1.0f;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-        if (on[b]) f *= move_refs(st, fmaxf(top[b], __shfl_xor(top[b], 32)), ev[b]);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] *= f;
+    const float ma = top_of(sa) * ka, mb = top_of(sb) * kb;
+    if (__any(passes(st, ma, va) || passes(st, mb, vb))) {
+      move(ma, va);
+      move(mb, vb);
     }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (!on[b]) continue;
-      f16x8 w[2];
-      weigh<16>(st, s[b], mul[b], ev[b], w);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(s_v[buf][b][64 * (k * (D / 32) + d) + lane], w[k], o[d], 0, 0, 0);
-    }
+    values(s_v[buf][0], sa, ka, va);
+    values(s_v[buf][1], sb, kb, vb);
   };
 
   if (job.begin < job.end) {
-    TileMeta cur, nxt;
-    fetch(job.begin, cur);
+    Tile cur = fetch(job.begin), nxt = cur;
     stage(0, cur);
-    if (job.begin + 1 < job.end) fetch(job.begin + 1, nxt);
+    if (job.begin + 1 < job.end) nxt = fetch(job.begin + 1);
     __syncthreads();
     for (int t = job.begin; t < job.end; ++t) {
       const int buf = (t - job.begin) & 1;
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
       if (t + 1 < job.end) {
         stage(buf ^ 1, nxt);
         cur = nxt;
-        if (t + 2 < job.end) fetch(t + 2, nxt);
+        if (t + 2 < job.end) nxt = fetch(t + 2);
       }
       __syncthreads();
     }
