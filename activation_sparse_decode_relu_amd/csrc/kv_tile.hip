@@ -109,48 +109,57 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     for (int e = 0; e < 16; ++e) o[d][e] = 0.0f;
 
   // ---- tiles: memory -> registers -> LDS -----------------------------------------------------------------
-  int vpage = -1, vslot = 0, vblk = 0, vexps = 0, window0 = 0, window1 = 0;   // lane k: block window0 + k of the span
+  // A thread carries the same unit of every block: its place in memory and in LDS is worked out once.
+  int vexps = -1, vblk = 0, window0 = 0, window1 = 0;   // lane k: block window0 + k of the span
+  size_t voff = 0;
   u32x4 codes[kMine];
+  const int unit = tid % kUnits, side = kUnits < kTileThreads ? wave / (kTileWaves / 2) : 0;
+  int k_to, v_to;
+  {
+    const int t = unit / D, chunk = (unit / 16) % (D / 16), rr = unit % 16;
+    k_to = 2 * chunk * 32 + 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);   // the row where the token's scores shall come out
+    const int p = unit / 64, g = (unit / 16) % 4;
+    v_to = ((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + unit % 16;
+  }
   auto fetch = [&](int tile) {
     if (2 * tile >= window1) {
       window0 = 2 * tile;
       window1 = window0 + WAVE;
       const int bi = window0 + lane;
-      vpage = -1;
-      vslot = vblk = vexps = 0;
+      vexps = -1;
+      vblk = 0;
+      voff = 0;
       if (bi < min(job.span.count(), 2 * job.end)) {
         vblk = job.span.block(bi);
-        vpage = kv_page(c, job.s.seq, vblk);
-        vslot = vblk % c.page_blocks;
-        if (vpage >= 0) {
-          const size_t e = block_at(c, vpage, head, vslot);
+        const int page = kv_page(c, job.s.seq, vblk);
+        if (page >= 0) {
+          const size_t e = block_at(c, page, head, vblk % c.page_blocks);
           vexps = (int)c.k_exp[e] | (int)c.v_exp[e] << 8;
+          voff = e * (kKvBlock * D);
         }
       }
     }
     const int k = 2 * tile - window0;
-    const int pa = __builtin_amdgcn_readlane(vpage, k), pb = __builtin_amdgcn_readlane(vpage, k + 1);
-    const size_t ea = block_at(c, max(pa, 0), head, __builtin_amdgcn_readlane(vslot, k)) * (kKvBlock * D);
-    const size_t eb = block_at(c, max(pb, 0), head, __builtin_amdgcn_readlane(vslot, k + 1)) * (kKvBlock * D);
+    auto lane_of = [&](int v, int i) { return __builtin_amdgcn_readlane(v, i); };
+    auto off = [&](int i) {
+      return (size_t)(unsigned)lane_of((int)(unsigned)voff, i) | (size_t)(unsigned)lane_of((int)(voff >> 32), i) << 32;
+    };
+    const size_t at[2] = {off(k), off(k + 1)};
 #pragma unroll
     for (int e = 0; e < kMine; ++e) {
-      const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
-      const uint8_t* p = (sec < 2 ? c.k : c.v) + ((sec & 1) ? eb : ea);
-      codes[e] = *(reinterpret_cast<const u32x4*>(p) + w);
+      const uint8_t* p = (e < kMine / 2 ? c.k : c.v) + (kMine == 4 ? at[e & 1] : side ? at[1] : at[0]);
+      codes[e] = *(reinterpret_cast<const u32x4*>(p) + unit);
     }
-    return Tile{__builtin_amdgcn_readlane(vblk, k) * kKvBlock, __builtin_amdgcn_readlane(vblk, k + 1) * kKvBlock,
-                pa < 0 ? -1 : __builtin_amdgcn_readlane(vexps, k), pb < 0 ? -1 : __builtin_amdgcn_readlane(vexps, k + 1)};
+    return Tile{lane_of(vblk, k) * kKvBlock, lane_of(vblk, k + 1) * kKvBlock, lane_of(vexps, k), lane_of(vexps, k + 1)};
   };
-  // this thread's pieces, decoded, to their places
+  // this thread's units, decoded, to their places
   auto stage = [&](int buf, const Tile& m) {
     // V's codes of tokens that are not there may be anything, and their weight of 0 is not enough
     if (m.xa < 0 || m.xb < 0 || max(m.ta, m.tb) + kKvBlock > job.s.len) {
 #pragma unroll
-      for (int e = 0; e < kMine; ++e) {
-        const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
-        if (sec < 2) continue;
-        const int t0 = (sec & 1) ? m.tb : m.ta, ex = (sec & 1) ? m.xb : m.xa;
-        const int left = ex < 0 ? 0 : min(max(job.s.len - (t0 + 8 * ((w / 16) % 4)), 0), 8);
+      for (int e = kMine / 2; e < kMine; ++e) {
+        const bool b = kMine == 4 ? e & 1 : side != 0;
+        const int left = (b ? m.xb : m.xa) < 0 ? 0 : min(max(job.s.len - ((b ? m.tb : m.ta) + 8 * ((unit / 16) % 4)), 0), 8);
         const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
         const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
         codes[e] &= u32x4{lo, hi, lo, hi};
@@ -158,14 +167,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     }
 #pragma unroll
     for (int e = 0; e < kMine; ++e) {
-      const int u = e * kTileThreads + tid, sec = __builtin_amdgcn_readfirstlane(u / kUnits), w = u % kUnits;
-      const int t = w / D, chunk = (w / 16) % (D / 16), rr = w % 16;
-      const int row = 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);   // where the token's scores shall come out
-      const int p = w / 64, g = (w / 16) % 4, dl = w % 16;
-      f16x8* to = sec < 2 ? &s_k[buf][sec & 1][2 * chunk * 32 + row]
-                          : &s_v[buf][sec & 1][((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + dl];
+      const int b = kMine == 4 ? e & 1 : side;
+      f16x8* to = e < kMine / 2 ? &s_k[buf][b][k_to] : &s_v[buf][b][v_to];
       to[0] = decode8<CODE>(codes[e].x, codes[e].y);
-      to[sec < 2 ? 32 : 16] = decode8<CODE>(codes[e].z, codes[e].w);
+      to[e < kMine / 2 ? 32 : 16] = decode8<CODE>(codes[e].z, codes[e].w);
     }
   };
   // scores of a block: register e of the lane is token t0 + 16 (e / 8) + 8 h + e % 8
