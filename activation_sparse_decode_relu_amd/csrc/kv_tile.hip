@@ -205,11 +205,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
       for (int d = 0; d < D / 32; ++d)
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[64 * (k * (D / 32) + d) + lane], w[k], o[d], 0, 0, 0);
   };
-  auto move = [&](float top, float ev) {
-    const float f = move_refs(st, fmaxf(top, __shfl_xor(top, 32)), ev);
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) o[d] *= f;
-  };
   // does a row of this wave see the block; do all of them see all of it
   auto seen = [&](int t0, int ex) {
     return ex >= 0 && t0 <= wp1 && (A.window == 0 || t0 < A.sinks || t0 + kKvBlock - 1 > wp0 - A.window);
@@ -228,8 +223,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     }
     const float ma = top_of(sa) * ka, mb = top_of(sb) * kb;
     if (__any(passes(st, ma, va) || passes(st, mb, vb))) {
-      move(ma, va);
-      move(mb, vb);
+      float f = move_refs(st, fmaxf(ma, __shfl_xor(ma, 32)), va);
+      f *= move_refs(st, fmaxf(mb, __shfl_xor(mb, 32)), vb);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] *= f;
     }
     values(s_v[buf][0], sa, ka, va);
     values(s_v[buf][1], sb, kb, vb);
