@@ -1,17 +1,22 @@
 // Attention of many rows: prompts, and pieces of prompts over what earlier pieces left.
 //
-// Bound by the matrix instructions and, as much, by the exponentials: a row and token costs 4 D operations of
-// the one and one of the other.  A workgroup takes 128 rows (query heads of a cached head times tokens),
-// four waves of 32, and passes over the tokens they see in tiles of 64.  The codes of a tile are
-// decoded once, to fp16 operands in LDS that every wave reads in whole lines (the 32x32x16 fragments,
-// lane after lane), into one of two buffers while the other is being used; the next tile's codes are on
-// their way from memory meanwhile.  Scores, softmax and output never leave the registers (kv_softmax.h).
-// Tiles that no row of a wave sees are skipped, and only those at the diagonal or at a window's edge
-// are masked.
+// Bound by the matrix instructions and, as much, by the vector ALU: a row and token costs 4 D operations of the one
+// and, of the other, an exponential and about six more (scale, maximum, sum, rounding, its share of the decoding).
+// A workgroup takes 128 rows (query heads of a cached head times tokens), four waves of 32, and passes over the
+// tokens they see in tiles of two blocks.  The codes of a tile are decoded once, to fp16 operands in LDS that every
+// wave reads in whole lines (the 32x32x16 fragments, lane after lane), into one of two buffers while the other is being
+// used; the next tile's codes are on their way from memory meanwhile.  Scores, softmax and output never leave the
+// registers (kv_softmax.h).  The scores of one block are computed beside the exponentials of the block before.  Only
+// blocks at the diagonal or at a window's edge are masked.
 //
-// Workgroups that read the same cached head stand kv_heads apart, so with 8 heads or a multiple they share
-// an L2, and the longest rows come first.  With few workgroups the tokens are split over several of
-// them; their states (fp32) are joined by a second kernel.
+// Workgroups that read the same cached head stand kv_heads apart, so with 8 heads or a multiple they share an L2,
+// and the longest rows come first.  With few workgroups the tokens are split over several of them; their states
+// (fp32) are joined by a second kernel.
+//
+// Measured, a prompt of 4096 with 64 query heads on 8: 320 us, 859 TFLOP/s (a library matrix product of 8192 runs at
+// 1155), the matrix instructions busy 38 % of the time and the vector ALU 50 %.  One workgroup a compute unit
+// instead of two takes 440 us; three, with blocks of 32 tokens in turn so that the registers suffice, 322.  Raising
+// a wave's priority in its products, or interleaving these with the exponentials one by one, was 1 to 6 % slower.
 #include "kv_softmax.h"
 
 namespace pik {
@@ -35,9 +40,30 @@ struct TileJob {
   __device__ __forceinline__ int pos(int r, int group) const { return p0 + r / group; }
 };
 
+// Up to 64 sequences: which of them owns `slot`, and its tile of rows, in the order in which the card is best
+// kept busy to the end: the longest sequences first and each one's last rows first.
+__device__ __forceinline__ int sorted_owner(const KvAttendArgs& A, int slot, int& local) {
+  const int lane = threadIdx.x & (WAVE - 1), i = min(lane, A.c.n - 1);
+  auto lane_of = [](int v, int k) { return __builtin_amdgcn_readlane(v, k); };
+  auto at = [&](int k) { return (int)((long long)min(max(A.c.starts[k], 0), A.c.rows) * A.group / kTileRows); };
+  const int count = max(at(i + 1) + 1 - at(i), 0), len = kv_seq(A.c, i).len;
+  int before = 0;
+  for (int k = 0; k < A.c.n; ++k) {
+    const int other = lane_of(len, k);
+    before += other > len || (other == len && k < lane) ? lane_of(count, k) : 0;
+  }
+  const unsigned long long mine = __ballot(lane < A.c.n && slot >= before && slot < before + count);
+  if (mine == 0) return -1;
+  const int owner = __builtin_ctzll(mine);
+  local = lane_of(count, owner) - 1 - (slot - lane_of(before, owner));
+  return owner;
+}
+
 __device__ __forceinline__ bool tile_job(const KvAttendArgs& A, int slot, int split, TileJob& j) {
   int local;
-  const int i = slot_owner(A.c, slot, A.group, kTileRows, 1, local);
+  const int i = A.c.n <= WAVE ? sorted_owner(A, slot, local)
+                              : slot_owner(A.c, A.slots - 1 - slot, A.group, kTileRows, 1, local);
+  if (i < 0) return false;
   j.s = kv_seq(A.c, i);
   j.R = min(j.s.rows, A.max_new) * A.group;
   j.r0 = local * kTileRows;
@@ -56,6 +82,7 @@ __device__ __forceinline__ bool tile_job(const KvAttendArgs& A, int slot, int sp
 // The two blocks of a tile: first token and exponents (K's, V's << 8), the latter -1 where there is no page.
 struct Tile {
   int ta, tb, xa, xb;
+  size_t oa, ob;        // where the blocks' codes begin
 };
 
 template <int ACT, int CODE, int D>
@@ -70,7 +97,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
   const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int col = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % c.kv_heads, rest = blockIdx.x / c.kv_heads;
-  const int split = rest % A.splits, slot = A.slots - 1 - rest / A.splits;
+  const int split = rest % A.splits, slot = rest / A.splits;
   TileJob job;
   if (!tile_job(A, slot, split, job)) return;
 
@@ -112,7 +139,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
   // A thread carries the same unit of every block: its place in memory and in LDS is worked out once.
   int vexps = -1, vblk = 0, window0 = 0, window1 = 0;   // lane k: block window0 + k of the span
   size_t voff = 0;
-  u32x4 codes[kMine];
+  u32x4 kc[kMine / 2], vc[kMine / 2];
   const int unit = tid % kUnits, side = kUnits < kTileThreads ? wave / (kTileWaves / 2) : 0;
   int k_to, v_to;
   {
@@ -121,7 +148,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     const int p = unit / 64, g = (unit / 16) % 4;
     v_to = ((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + unit % 16;
   }
-  auto fetch = [&](int tile) {
+  auto find = [&](int tile) {
     if (2 * tile >= window1) {
       window0 = 2 * tile;
       window1 = window0 + WAVE;
@@ -144,33 +171,40 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
     auto off = [&](int i) {
       return (size_t)(unsigned)lane_of((int)(unsigned)voff, i) | (size_t)(unsigned)lane_of((int)(voff >> 32), i) << 32;
     };
-    const size_t at[2] = {off(k), off(k + 1)};
-#pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      const uint8_t* p = (e < kMine / 2 ? c.k : c.v) + (kMine == 4 ? at[e & 1] : side ? at[1] : at[0]);
-      codes[e] = *(reinterpret_cast<const u32x4*>(p) + unit);
-    }
-    return Tile{lane_of(vblk, k) * kKvBlock, lane_of(vblk, k + 1) * kKvBlock, lane_of(vexps, k), lane_of(vexps, k + 1)};
+    return Tile{lane_of(vblk, k) * kKvBlock, lane_of(vblk, k + 1) * kKvBlock, lane_of(vexps, k), lane_of(vexps, k + 1),
+                off(k), off(k + 1)};
   };
-  // this thread's units, decoded, to their places
-  auto stage = [&](int buf, const Tile& m) {
-    // V's codes of tokens that are not there may be anything, and their weight of 0 is not enough
+  // this thread's units of two blocks: on their way from memory, and, decoded, to their places
+  auto fetch = [&](const uint8_t* base, size_t first, size_t second, u32x4* to) {
+#pragma unroll
+    for (int e = 0; e < kMine / 2; ++e)
+      to[e] = *(reinterpret_cast<const u32x4*>(base + (kMine == 4 ? (e ? second : first) : side ? second : first)) + unit);
+  };
+  auto stage_k = [&](f16x8* first, f16x8* second) {
+#pragma unroll
+    for (int e = 0; e < kMine / 2; ++e) {
+      f16x8* to = (kMine == 4 ? (e ? second : first) : side ? second : first) + k_to;
+      to[0] = decode8<CODE>(kc[e].x, kc[e].y);
+      to[32] = decode8<CODE>(kc[e].z, kc[e].w);
+    }
+  };
+  auto stage_v = [&](int buf, const Tile& m) {
+    // codes of tokens that are not there may be anything, and their weight of 0 is not enough
     if (m.xa < 0 || m.xb < 0 || max(m.ta, m.tb) + kKvBlock > job.s.len) {
 #pragma unroll
-      for (int e = kMine / 2; e < kMine; ++e) {
-        const bool b = kMine == 4 ? e & 1 : side != 0;
+      for (int e = 0; e < kMine / 2; ++e) {
+        const bool b = kMine == 4 ? e != 0 : side != 0;
         const int left = (b ? m.xb : m.xa) < 0 ? 0 : min(max(job.s.len - ((b ? m.tb : m.ta) + 8 * ((unit / 16) % 4)), 0), 8);
         const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
         const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
-        codes[e] &= u32x4{lo, hi, lo, hi};
+        vc[e] &= u32x4{lo, hi, lo, hi};
       }
     }
 #pragma unroll
-    for (int e = 0; e < kMine; ++e) {
-      const int b = kMine == 4 ? e & 1 : side;
-      f16x8* to = e < kMine / 2 ? &s_k[buf][b][k_to] : &s_v[buf][b][v_to];
-      to[0] = decode8<CODE>(codes[e].x, codes[e].y);
-      to[e < kMine / 2 ? 32 : 16] = decode8<CODE>(codes[e].z, codes[e].w);
+    for (int e = 0; e < kMine / 2; ++e) {
+      f16x8* to = &s_v[buf][kMine == 4 ? e : side][v_to];
+      to[0] = decode8<CODE>(vc[e].x, vc[e].y);
+      to[16] = decode8<CODE>(vc[e].z, vc[e].w);
     }
   };
   // scores of a block: register e of the lane is token t0 + 16 (e / 8) + 8 h + e % 8
@@ -205,48 +239,62 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
       for (int d = 0; d < D / 32; ++d)
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[64 * (k * (D / 32) + d) + lane], w[k], o[d], 0, 0, 0);
   };
-  // does a row of this wave see the block; do all of them see all of it
-  auto seen = [&](int t0, int ex) {
-    return ex >= 0 && t0 <= wp1 && (A.window == 0 || t0 < A.sinks || t0 + kKvBlock - 1 > wp0 - A.window);
-  };
+  // do all rows of this wave see all of the block
   auto whole = [&](int t0, int ex) {
     return ex >= 0 && t0 + kKvBlock - 1 <= wp0 && (A.window == 0 || t0 > wp1 - A.window);
   };
-  auto compute = [&](int buf, const Tile& m) {
-    const float ka = score_factor(row_mul, max((m.xa & 255) - 127, -126)), kb = score_factor(row_mul, max((m.xb & 255) - 127, -126));
-    const float va = (float)max(((m.xa >> 8) & 255) - 127, -126), vb = (float)max(((m.xb >> 8) & 255) - 127, -126);
-    if (!seen(m.ta, m.xa) && !seen(m.tb, m.xb)) return;
-    f32x16 sa = scores(s_k[buf][0]), sb = scores(s_k[buf][1]);
-    if (!whole(m.ta, m.xa) || !whole(m.tb, m.xb)) {
-      mask(sa, m.ta, m.xa);
-      mask(sb, m.tb, m.xb);
-    }
-    const float ma = top_of(sa) * ka, mb = top_of(sb) * kb;
-    if (__any(passes(st, ma, va) || passes(st, mb, vb))) {
-      float f = move_refs(st, fmaxf(ma, __shfl_xor(ma, 32)), va);
-      f *= move_refs(st, fmaxf(mb, __shfl_xor(mb, 32)), vb);
+  // One block: its scores `s` are there already; those of the block after it are computed beside its exponentials,
+  // so that the matrix instructions and the vector ALU work at the same time.
+  auto step = [&](int t0, int ex, f32x16& s, const f16x8* v, f32x16& next, const f16x8* k) {
+    if (!whole(t0, ex)) mask(s, t0, ex);
+    const float mul = score_factor(row_mul, max((ex & 255) - 127, -126)), ev = (float)max(((ex >> 8) & 255) - 127, -126);
+    const float top = top_of(s) * mul;
+    if (__any(passes(st, top, ev))) {
+      const float f = move_refs(st, fmaxf(top, __shfl_xor(top, 32)), ev);
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) o[d] *= f;
     }
-    values(s_v[buf][0], sa, ka, va);
-    values(s_v[buf][1], sb, kb, vb);
+    next = scores(k);
+    values(v, s, mul, ev);
   };
-
   if (job.begin < job.end) {
-    Tile cur = fetch(job.begin), nxt = cur;
-    stage(0, cur);
-    if (job.begin + 1 < job.end) nxt = fetch(job.begin + 1);
+    // tiles t, t + 1 and t + 2.  K is staged a block further ahead than V: the pair that is on its way is block b of one
+    // tile and block a of the next.
+    Tile cur = find(job.begin), nxt = find(job.begin + 1), far = find(job.begin + 2);
+    fetch(c.k, cur.oa, cur.ob, kc);
+    fetch(c.v, cur.oa, cur.ob, vc);
+    stage_k(s_k[0][0], s_k[0][1]);
+    fetch(c.k, nxt.oa, nxt.oa, kc);
+    stage_k(s_k[1][0], s_k[1][0]);
+    stage_v(0, cur);
+    fetch(c.k, nxt.ob, far.oa, kc);
+    fetch(c.v, nxt.oa, nxt.ob, vc);
     __syncthreads();
-    for (int t = job.begin; t < job.end; ++t) {
-      const int buf = (t - job.begin) & 1;
-      compute(buf, cur);
-      if (t + 1 < job.end) {
-        stage(buf ^ 1, nxt);
-        cur = nxt;
-        if (t + 2 < job.end) nxt = fetch(t + 2);
+    f32x16 sa = scores(s_k[0][0]), sb;
+    __syncthreads();                        // every wave is past them before tile 2 takes their place
+    auto advance = [&](int t, int buf) {
+      stage_k(s_k[buf ^ 1][1], s_k[buf][0]);
+      stage_v(buf ^ 1, nxt);
+      cur = nxt;
+      nxt = far;
+      if (t + 2 < job.end) {
+        far = find(t + 3);
+        fetch(c.k, nxt.ob, far.oa, kc);
+        fetch(c.v, nxt.oa, nxt.ob, vc);
       }
       __syncthreads();
+    };
+    // the tiles up to the last that a row of this wave sees
+    const int seen = wp1 < 0 ? 0 : (job.span.sink + max(wp1 / kKvBlock - job.span.from, 0)) / 2 + 1;
+    const int stop = min(max(seen, job.begin), job.end);
+    int t = job.begin;
+    for (; t < stop; ++t) {
+      const int buf = (t - job.begin) & 1;
+      step(cur.ta, cur.xa, sa, s_v[buf][0], sb, s_k[buf][1]);
+      step(cur.tb, cur.xb, sb, s_v[buf][1], sa, s_k[buf ^ 1][0]);
+      advance(t, buf);
     }
+    for (; t < job.end; ++t) advance(t, (t - job.begin) & 1);
   }
 
   // ---- out: register 4 a + e of o[d] is dim 32 d + 8 a + 4 h + e ---------------------------------------
