@@ -53,9 +53,10 @@ struct KvAttendArgs {
 // Few rows of a cached head (max_new * group up to kStepRows): step_groups workgroups, as many as the card holds
 // at once, each with an equal stretch of the call's blocks, in grains of kStepGrain.
 constexpr int kStepRows = 64, kStepGrain = 8;
-// tiles: 16-row tiles a wave holds.  Two to four workgroups a compute unit, by the registers these take.
+// tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.
+constexpr int step_waves(int tiles, int dim) { return tiles == 4 && dim == 64 ? 8 : 4; }
 constexpr int step_groups(int tiles, int dim) {
-  return 256 * (tiles == 1 ? (dim == 64 ? 4 : 3) : tiles == 4 && dim == 128 ? 1 : 2);
+  return 256 * (tiles == 1 ? (dim == 64 ? 4 : 3) : tiles == 4 ? 1 : 2);
 }
 // Pieces a call's items (sequences times cached heads) are cut into at most, and workgroups it is launched with
 // at most.  Those of items that are cut leave a part each: at most 2 * step_groups.

@@ -27,8 +27,6 @@ namespace pik {
 
 namespace {
 
-constexpr int kWaves = 4;
-
 // What one sequence brings to the call, as a lane holds it.
 struct StepSeq {
   int seq, len, row0, rows;   // rows: those computed, at most max_new
@@ -84,14 +82,14 @@ constexpr int kFan = 8;
 __device__ __forceinline__ int fan_of(int parts) { return parts <= kFan ? parts : (int)ceilf(sqrtf((float)parts)); }
 
 // The joined state of `n` parts (slots from, from + step, ... of the workspace) of R rows; sink(r, d, v, state) gets four dims of a row's O' and its state.
-template <int D, int kRows, class Sink>
+template <int D, int kRows, int kWaves, class Sink>
 __device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* lds, int from, int step, int n, int R,
                                            Sink&& sink) {
   constexpr int kRow = D + 4;
   f32x4* state = reinterpret_cast<f32x4*>(lds);          // [n + 1][kRows]: the last is the joined one
   auto word = [&](int i, int r) { return ((from + i * step) * kRows + r) * kRow; };
   // every load of a batch of parts is on its way before the first is used, the first batch before the states
-  constexpr int kThreads = WAVE * kWaves, kMine = kRows * (D / 4) / kThreads, kBatch = 16 / kMine;
+  constexpr int kThreads = WAVE * kWaves, kMine = kRows * (D / 4) / kThreads, kBatch = (kRows == 64 ? 32 : 16) / kMine;
   f32x4 y[kMine][kBatch], v[kMine];
   auto batch = [&](int i0) {
 #pragma unroll
@@ -159,10 +157,10 @@ __device__ __forceinline__ bool last_of(unsigned* ticket, int n, int* s_last) {
 }
 
 template <int ACT, int CODE, int D, int NT>
-__global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_step(const KvAttendArgs A) {
+__global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_waves(NT, D) / 1024) void k_kv_step(const KvAttendArgs A) {
   using T = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
-  constexpr int kRows = 16 * NT, kRow = D + 4;        // rows of a tile; floats of a row's partial
+  constexpr int kWaves = step_waves(NT, D), kRows = 16 * NT, kRow = D + 4;        // rows of a tile; floats of a row's partial
   __shared__ float s_part[kWaves][kRows][kRow];       // O', then rr, mm, l
   __shared__ int s_last;
   const KvView& c = A.c;
@@ -428,12 +426,12 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
       if (last_of(A.tickets + w0, m, &s_last)) {
         float* lds = &s_part[0][0][0];
         if (groups == 1) {
-          join_parts<D, kRows>(prs, lds, first, 1, m, R, store_row);
+          join_parts<D, kRows, kWaves>(prs, lds, first, 1, m, R, store_row);
         } else {
-          join_parts<D, kRows>(prs, lds, w0, 1, m, R,
+          join_parts<D, kRows, kWaves>(prs, lds, w0, 1, m, R,
                                [&](int r, int d, const f32x4& v, const RowState& a) { store_part(w0, r, d, v, a); });
           if (last_of(A.tickets + kStepTickets / 2 + first, groups, &s_last))
-            join_parts<D, kRows>(prs, lds, first, fan, groups, R, store_row);
+            join_parts<D, kRows, kWaves>(prs, lds, first, fan, groups, R, store_row);
         }
       }
     }
@@ -443,7 +441,7 @@ __global__ __launch_bounds__(WAVE* kWaves, step_groups(NT, D) / 256) void k_kv_s
 
 template <int ACT, int CODE, int D, int NT>
 hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(step_groups(NT, D), a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * kWaves), 0, s, a);
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(step_groups(NT, D), a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * step_waves(NT, D)), 0, s, a);
   return hipGetLastError();
 }
 
