@@ -109,9 +109,11 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   if (tid == 0) s_failed = 0;
   // how many pages the call wants in all
   int want = 0;
+  Need mine{0, 0, 0, 0, 0, -1};          // of the first kPlan sequences: seldom are there more
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
     const Need r = i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1};
+    if (base == 0) mine = r;
     int total;
     block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
     want = min(want + total, P.pages + 1);   // more than there are is as good as one too many
@@ -124,7 +126,7 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   int given = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    Need r = i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1};
+    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1};
     int total;
     const int at = given + block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
     const bool grows = i < n && r.pages >= 0 && at + r.pages <= found;
