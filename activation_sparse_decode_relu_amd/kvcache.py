@@ -221,7 +221,7 @@ class KVCache:
 
     def _stream(self, stream, tensors) -> int:
         if stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream or None
+            return torch.cuda.current_stream(self.device.index).cuda_stream or None
         for t in tensors:   # memory the caller lets go of stays theirs until this stream is past the call
             if t is not None:
                 t.record_stream(stream)
