@@ -50,21 +50,32 @@ struct KvAttendArgs {
   unsigned* tickets;   // workspace: kStepTickets counters, zero between calls
 };
 
-// Few rows of a cached head (max_new * group up to kStepRows): step_groups workgroups, as many as the card holds
-// at once, each with an equal stretch of the call's blocks, in grains of kStepGrain.
+// Few rows of a cached head (max_new * group up to kStepRows): items (sequences times cached heads) in pieces, one
+// workgroup each, see kv_step.hip.  S is at least kStepGrain blocks.
 constexpr int kStepRows = 64, kStepGrain = 8;
-// tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.
+// tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.  Eight
+// waves instead of four where 33 to 64 rows have 64 dims: half as many parts to join (four tokens over 100003, 16
+// query heads to a cached one: 46.0 against 50.5 us); with 128 dims LDS does not hold eight waves' parts.
 constexpr int step_waves(int tiles, int dim) { return tiles == 4 && dim == 64 ? 8 : 4; }
 constexpr int step_groups(int tiles, int dim) {
   return 256 * (tiles == 1 ? (dim == 64 ? 4 : 3) : tiles == 4 ? 1 : 2);
 }
-// Pieces a call's items (sequences times cached heads) are cut into at most, and workgroups it is launched with
-// at most.  Those of items that are cut leave a part each: at most 2 * step_groups.
-constexpr int step_pieces(int groups, int items) { return items + groups / 2 > groups ? items + groups / 2 : groups; }
-constexpr int kStepLaunch = 4096, kStepTickets = 2 * 2048;
+// The smallest S is the call's blocks over step_shares, and the pieces are at most step_pieces.  With one row tile two
+// workgroups a compute unit stream as fast as three or four, and fewer parts have to be joined: up to 512 pieces
+// instead of 768 took 44.8 against 50.4 us (one sequence of 100003), 22.4 against 24.5 (four of 8000), 27.1 against
+// 32.5 (64 of 2000, 64 dims).  Many items of uneven length, though, end sooner in more pieces: 64 of 100 to 8192,
+// 512 items, 66.8 us in up to 896 pieces against 68.5 in 768.
+constexpr int step_shares(int tiles, int dim) { return tiles == 1 ? 768 : step_groups(tiles, dim); }
+constexpr int step_pieces(int tiles, int dim, int items) {
+  const int least = tiles == 1 ? 512 : step_groups(tiles, dim), most = items + step_shares(tiles, dim) / 2;
+  return most > least ? most : least;
+}
+// Workgroups a call is launched with at most.  The pieces of items that are cut leave a part each: at most
+// 2 * step_shares, so many tickets and places in the workspace there are.
+constexpr int kStepLaunch = 4096, kStepTickets = 2 * 2 * 768;
 constexpr size_t step_partial_floats(int dim) { return (size_t)2 * 512 * kStepRows * (dim + 4); }
-static_assert(step_groups(1, 64) * 16 <= 512 * kStepRows && step_groups(1, 128) * 16 <= 512 * kStepRows &&
-              step_groups(2, 64) * 32 <= 512 * kStepRows && step_groups(1, 64) <= kStepTickets / 4, "workspace");
+static_assert(768 * 16 <= 512 * kStepRows && step_groups(2, 64) * 32 <= 512 * kStepRows &&
+              step_groups(4, 64) * 64 <= 512 * kStepRows && step_groups(2, 128) <= 768, "workspace");
 hipError_t launch_kv_step(int act, int code, const KvAttendArgs& a, hipStream_t s);
 // Any number of rows, kTileRows a workgroup; where that leaves fewer than kTileParts / 2 workgroups, the
 // tokens of each are split over up to kTileParts in all.

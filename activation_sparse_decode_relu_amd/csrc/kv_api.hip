@@ -262,7 +262,13 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
   a.scale = args->scale;
   a.partial = reinterpret_cast<float*>(h->ws + h->L.partial);
   a.tickets = reinterpret_cast<unsigned*>(h->ws + h->L.tickets);
-  if ((int64_t)a.max_new * a.group <= pik::kStepRows) {
+  // Rows of a cached head for which the codes go straight to the matrix instructions; more go through LDS.  33 to 64
+  // rows of 128 dims are slow there (one workgroup a compute unit, and large parts to join), which pays only where
+  // there are items enough: eight tokens on one head of eight query heads, sequences of 4000, took 34.9 us against
+  // 24.1 through LDS with 16 items, 36.4 against 31.1 with 32, 41.2 against 41.8 with 64 and 56 against 82 with 128.
+  // With 64 dims, four tokens of 16 query heads, 48.6 against 62.7 us over 100003 tokens, 18.1 against 14.2 over 2000.
+  const int64_t shared = (int64_t)a.max_new * a.group, items = (int64_t)a.c.n * a.c.kv_heads;
+  if (shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32)) {
     // the kernel counts the call's blocks of 32 tokens in 32 bits
     const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
     const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + a.max_new) / PI_KV_BLOCK + 4) : cap;

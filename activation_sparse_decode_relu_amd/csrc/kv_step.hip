@@ -1,12 +1,12 @@
 // Attention of few rows: single tokens and a handful (up to 64 rows of a cached head), over long caches.
 //
 // Bound by reading the codes.  An item is a sequence and cached head with its blocks of 32 tokens; items are cut
-// into pieces of up to S blocks, one workgroup each, so that the card is filled once: S is the smallest of five
-// sizes from (blocks of the call) / (workgroups the card holds) to twice that which gives no more pieces than
-// fit, or, with many items, half a round more than there are items.  Every workgroup works this out by itself
-// from the lengths (they are on the device).  Starting a piece costs as much as some 8 blocks (its lengths, pages
-// and codes are loads that wait for each other), so whole items are better than equal stretches of the call's
-// blocks: 64 sequences of 1000 tokens, 8 heads, took 36.4 us with equal stretches and take 27.3.
+// into pieces of up to S blocks, one workgroup each, so that the card is filled once: S is the smallest of five sizes
+// from (blocks of the call) / step_shares to twice that which gives no more than step_pieces.  Every workgroup
+// works this out by itself from the lengths (they are on the device).  Starting a piece costs as much as some 8
+// blocks (its lengths, pages and codes are loads that wait for each other), so whole items are better than equal
+// stretches of the call's blocks: 64 sequences of 1000 tokens, 8 heads, took 36.4 us with equal stretches and
+// take 27.1.
 //
 // The four waves of a workgroup take the blocks of a piece in turn, each with its own online softmax,
 // straight from memory to the matrix instructions' operands: a block's bytes are stored in their order, so
@@ -17,7 +17,7 @@
 // workspace and the last of them, by a ticket, joins the parts in their order, so the result does not depend
 // on who was last.
 //
-// Measured: long caches stream at 6.0 TB/s (64 x 4000 tokens, 526 MB in 87.7 us) and some 9 us go to the start
+// Measured: long caches stream at 6.1 TB/s (64 x 4000 tokens, 526 MB in 86.6 us) and some 9 us go to the start
 // and the end, in which nothing streams.
 #include <algorithm>
 
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
   const __amdgpu_buffer_rsrc_t prs = partial_rsrc(A.partial);
 
   // ---- the pieces: see the top of the file --------------------------------------------------------
-  constexpr int G = step_groups(NT, D), kTries = 5;
+  constexpr int G = step_shares(NT, D), kTries = 5;
   StepSeq mine = step_seq(A, lane);
   int sum = mine.blocks;
   for (int base = WAVE; base < c.n; base += WAVE) sum += step_seq(A, base + lane).blocks;
@@ -187,7 +187,7 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
 #pragma unroll
       for (int e = 0; e < kTries; ++e) got[e] += pieces_of(blocks, tries[e]);
     }
-    const int most = step_pieces(G, c.n * c.kv_heads);
+    const int most = step_pieces(NT, D, c.n * c.kv_heads);
 #pragma unroll
     for (int e = kTries - 1; e >= 0; --e)
       if (e == kTries - 1 || wave_total(got[e]) * c.kv_heads <= most) S = tries[e];
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
 
 template <int ACT, int CODE, int D, int NT>
 hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(step_groups(NT, D), a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * step_waves(NT, D)), 0, s, a);
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(NT, D, a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * step_waves(NT, D)), 0, s, a);
   return hipGetLastError();
 }
 
