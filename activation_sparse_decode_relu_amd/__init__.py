@@ -1,7 +1,7 @@
-"""Activation-sparse ReLU FFN decode on MI355X (gfx950).
+"""Activation-sparse ReLU FFN decode, and attention over an 8-bit paged cache, on MI355X (gfx950).
 
-The compute lives in libpi_ffn.so (hand-written HIP kernels behind the C ABI in
-include/pi_ffn.h); this package is its thin Python binding.
+The compute lives in libpi_ffn.so (hand-written HIP kernels behind the C ABIs in
+include/pi_ffn.h and include/pi_kv.h); this package is its thin Python binding.
 """
 
 from .binding import (  # noqa: F401

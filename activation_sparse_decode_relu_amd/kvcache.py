@@ -178,7 +178,7 @@ class KVCache:
             raise _invalid(f"{name} is on {t.device}, the cache is on {self.device}")
         if t.dtype is not dtype:
             raise _invalid(f"{name} is {t.dtype}, expected {dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise _invalid(f"{name} must be {list(shape)}, got {list(t.shape)}")
         if not t.is_contiguous():
             raise _invalid(f"{name} is not contiguous")
@@ -213,6 +213,8 @@ class KVCache:
 
     def _writable(self, t, name) -> None:
         """A tensor that a call writes may not be an expanded view: rows must not overlap."""
+        if t.is_contiguous():
+            return
         token, head, _ = t.stride()
         rows, heads, dim = t.shape
         a, b = ((token, rows), (head, heads)) if token <= head else ((head, heads), (token, rows))

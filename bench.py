@@ -128,9 +128,10 @@ def budget_rank(cfg, p, B: int, frac: float, step: int = 64) -> int:
 
 
 def source_hash() -> str:
+    """Of the sparse FFN's sources: the attention cache's (kv*) are not part of the timed step."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "activation_sparse_decode_relu_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
+    for name in sorted(n for n in os.listdir(csrc) if not n.startswith("kv")):
         with open(os.path.join(csrc, name), "rb") as f:
             h.update(name.encode() + f.read())
     return h.hexdigest()[:16]
