@@ -19,8 +19,6 @@
 //
 // Measured: long caches stream at 6.1 TB/s (64 x 4000 tokens, 526 MB in 86.6 us) and some 9 us go to the start
 // and the end, in which nothing streams.
-#include <algorithm>
-
 #include "kv_softmax.h"
 
 namespace pik {
@@ -81,7 +79,8 @@ __device__ __forceinline__ u32x4 codes_piece(__amdgpu_buffer_rsrc_t r, int piece
 constexpr int kFan = 8;
 __device__ __forceinline__ int fan_of(int parts) { return parts <= kFan ? parts : (int)ceilf(sqrtf((float)parts)); }
 
-// The joined state of `n` parts (slots from, from + step, ... of the workspace) of R rows; sink(r, d, v, state) gets four dims of a row's O' and its state.
+// The joined state of `n` parts (slots from, from + step, ... of the workspace) of R rows; sink(r, d, v, state)
+// gets four dims of a row's O' and its state.
 template <int D, int kRows, int kWaves, class Sink>
 __device__ __forceinline__ void join_parts(__amdgpu_buffer_rsrc_t prs, float* lds, int from, int step, int n, int R,
                                            Sink&& sink) {
@@ -157,10 +156,11 @@ __device__ __forceinline__ bool last_of(unsigned* ticket, int n, int* s_last) {
 }
 
 template <int ACT, int CODE, int D, int NT>
-__global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_waves(NT, D) / 1024) void k_kv_step(const KvAttendArgs A) {
+__global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_waves(NT, D) / 1024) void k_kv_step(
+    const KvAttendArgs A) {
   using T = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
-  constexpr int kWaves = step_waves(NT, D), kRows = 16 * NT, kRow = D + 4;        // rows of a tile; floats of a row's partial
+  constexpr int kWaves = step_waves(NT, D), kRows = 16 * NT, kRow = D + 4;   // rows of a tile; floats of a row's part
   __shared__ float s_part[kWaves][kRows][kRow];       // O', then rr, mm, l
   __shared__ int s_last;
   const KvView& c = A.c;
@@ -441,7 +441,8 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
 
 template <int ACT, int CODE, int D, int NT>
 hipError_t step_go(const KvAttendArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(std::min(step_pieces(NT, D, a.c.n * a.c.kv_heads), kStepLaunch)), dim3(WAVE * step_waves(NT, D)), 0, s, a);
+  hipLaunchKernelGGL((k_kv_step<ACT, CODE, D, NT>), dim3(step_launch(NT, D, a.c.n * a.c.kv_heads)),
+                     dim3(WAVE * step_waves(NT, D)), 0, s, a);
   return hipGetLastError();
 }
 

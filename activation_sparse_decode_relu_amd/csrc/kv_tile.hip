@@ -145,7 +145,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
   int k_to, v_to;
   {
     const int t = unit / D, chunk = (unit / 16) % (D / 16), rr = unit % 16;
-    k_to = 2 * chunk * 32 + 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);   // the row where the token's scores shall come out
+    // K: the row where the token's scores shall come out
+    k_to = 2 * chunk * 32 + 8 * (2 * (rr >> 3) + t) + 4 * ((rr >> 2) & 1) + (rr & 3);
     const int p = unit / 64, g = (unit / 16) % 4;
     v_to = ((((g >> 1) * (D / 32) + p) * 2) + (g & 1)) * 32 + unit % 16;
   }
@@ -178,8 +179,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
   // this thread's units of two blocks: on their way from memory, and, decoded, to their places
   auto fetch = [&](const uint8_t* base, size_t first, size_t second, u32x4* to) {
 #pragma unroll
-    for (int e = 0; e < kMine / 2; ++e)
-      to[e] = *(reinterpret_cast<const u32x4*>(base + (kMine == 4 ? (e ? second : first) : side ? second : first)) + unit);
+    for (int e = 0; e < kMine / 2; ++e) {
+      const size_t at = kMine == 4 ? (e ? second : first) : side ? second : first;
+      to[e] = *(reinterpret_cast<const u32x4*>(base + at) + unit);
+    }
   };
   auto stage_k = [&](f16x8* first, f16x8* second) {
 #pragma unroll
@@ -195,7 +198,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
 #pragma unroll
       for (int e = 0; e < kMine / 2; ++e) {
         const bool b = kMine == 4 ? e != 0 : side != 0;
-        const int left = (b ? m.xb : m.xa) < 0 ? 0 : min(max(job.s.len - ((b ? m.tb : m.ta) + 8 * ((unit / 16) % 4)), 0), 8);
+        const int first = (b ? m.tb : m.ta) + 8 * ((unit / 16) % 4);
+        const int left = (b ? m.xb : m.xa) < 0 ? 0 : min(max(job.s.len - first, 0), 8);
         const unsigned lo = left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
         const unsigned hi = left >= 8 ? ~0u : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
         vc[e] &= u32x4{lo, hi, lo, hi};

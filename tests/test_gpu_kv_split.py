@@ -75,3 +75,24 @@ def test_pages_past_two_gib():
     assert int(r.cache.table.max()) == int((r.cache.refs > 0).sum()) - 1
     r.check_stored()
     r.attend([1, 2, 1])
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), -float("inf")])
+@pytest.mark.parametrize("rows", [2, 90])
+def test_a_query_that_is_not_finite_stays_alone(rows, bad):
+    """One element of one query spoils its own output and no other's."""
+    announce(f"kv attend, query {bad}, {rows} rows")
+    r = Rig([400], 4, 2, 64, 32, "f16", "e4m3", seed=45)
+    r.append([400])
+    q = torch.from_numpy(1.5 * r.rng.standard_normal((rows, 4, 64))).half()
+    spoiled = q.clone()
+    spoiled[rows // 2, 1, 5] = bad
+    out = torch.full((rows, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.empty(rows, 4, device="cuda")
+    ids = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0], [0, rows])]
+    r.cache.attend(0, spoiled.cuda(), out, *ids, rows, lse=lse)
+    clean, clean_lse = torch.empty_like(out), torch.empty_like(lse)
+    r.cache.attend(0, q.cuda(), clean, *ids, rows, lse=clean_lse)
+    assert not bool(torch.isfinite(out[rows // 2, 1]).all())
+    out[rows // 2, 1], lse[rows // 2, 1] = clean[rows // 2, 1], clean_lse[rows // 2, 1]
+    r.compare(q, out, lse, [0, rows], [0], 0, 0, None)
