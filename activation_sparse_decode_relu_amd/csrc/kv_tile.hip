@@ -13,8 +13,8 @@
 // and the longest rows come first.  With few workgroups the tokens are split over several of them; their states
 // (fp32) are joined by a second kernel.
 //
-// Measured, a prompt of 4096 with 64 query heads on 8: 311 to 337 us on different cards, 816 to 884 TFLOP/s (a library
-// matrix product of 8192 runs at 1107 to 1155), the matrix instructions busy 38 % of the time and the vector ALU 50 %.
+// Measured, a prompt of 4096 with 64 query heads on 8: 306 to 337 us on different cards, 816 to 897 TFLOP/s (a library
+// matrix product of 8192 runs at 1107 to 1167), the matrix instructions busy 38 % of the time and the vector ALU 50 %.
 // One workgroup a compute unit instead of two took 440 us where this took 318; three, with blocks of 32 tokens in turn
 // so that the registers suffice, 322.  Raising a wave's priority in its products, or interleaving these with the
 // exponentials one by one, was 1 to 6 % slower.
