@@ -62,7 +62,8 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   if (end > (long long)P.max_pages * P.page_tokens) return r;
   r.end = (int)end;
   r.have = (r.len + P.page_tokens - 1) / P.page_tokens;
-  r.pages = min((r.end + P.page_tokens - 1) / P.page_tokens - r.have, P.pages);
+  // one more than there are is as good as any number that cannot be had, and keeps the call's sum in 32 bits
+  r.pages = min((r.end + P.page_tokens - 1) / P.page_tokens - r.have, P.pages + 1);
   if (c > 0 && r.len % P.page_tokens != 0) {
     const int last = P.table[(size_t)r.s * P.max_pages + r.have - 1];
     if (last < 0 || last >= P.pages) {
