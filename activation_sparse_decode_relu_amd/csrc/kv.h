@@ -34,6 +34,7 @@ struct KvStoreArgs {
   KvView c;
   KvRows k, v;
   const int* first;    // read: first token of each sequence, or NULL
+  const int* refused;  // append: the length, plus 1, at which reserve refused a sequence, else 0 [max_seqs]
 };
 hipError_t launch_kv_append(int act, int code, const KvStoreArgs& a, hipStream_t s);
 hipError_t launch_kv_read(int act, int code, const KvStoreArgs& a, hipStream_t s);
@@ -102,6 +103,7 @@ struct KvPool {
   int* lens;
   int* refs;
   int* failed;
+  int* refused;
   int* src;            // workspace: pages to copy from and to, -1 for none [max(pages, max_seqs)]
   int* dst;
   int* list;           // workspace: reserve's free pages, compact's new places [pages]

@@ -110,6 +110,7 @@ pik::KvPool pool_of(const pi_kv* h) {
   p.lens = h->buf.lens;
   p.refs = h->buf.refs;
   p.failed = h->buf.failed;
+  p.refused = h->buf.refused;
   p.src = reinterpret_cast<int*>(h->ws + h->L.src);
   p.dst = reinterpret_cast<int*>(h->ws + h->L.dst);
   p.list = reinterpret_cast<int*>(h->ws + h->L.list);
@@ -188,7 +189,8 @@ pi_status pi_kv_create(const pi_kv_desc* desc, const pi_kv_buffers* buffers, voi
     return fail(PI_ERR_INVALID, "k or v is NULL or not 16-byte aligned");
   if (buffers->k_exp == nullptr || buffers->v_exp == nullptr) return fail(PI_ERR_INVALID, "k_exp or v_exp is NULL");
   if ((st = check_ints(buffers->table, "table")) != PI_OK || (st = check_ints(buffers->lens, "lens")) != PI_OK ||
-      (st = check_ints(buffers->refs, "refs")) != PI_OK || (st = check_ints(buffers->failed, "failed")) != PI_OK)
+      (st = check_ints(buffers->refs, "refs")) != PI_OK || (st = check_ints(buffers->failed, "failed")) != PI_OK ||
+      (st = check_ints(buffers->refused, "refused")) != PI_OK)
     return st;
   const Layout L = layout_for(*desc);
   if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < L.total)
@@ -221,7 +223,7 @@ pi_status pi_kv_append(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv
   if (st != PI_OK) return st;
   if (batch->rows == 0) return ok();
   if ((st = check_rows(k, "k")) != PI_OK || (st = check_rows(v, "v")) != PI_OK) return st;
-  pik::KvStoreArgs a{view_of(h, layer, batch), rows_of(k), rows_of(v), nullptr};
+  pik::KvStoreArgs a{view_of(h, layer, batch), rows_of(k), rows_of(v), nullptr, h->buf.refused};
   return launched(pik::launch_kv_append(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "append");
 }
 
@@ -232,7 +234,7 @@ pi_status pi_kv_read(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_r
   if (first != nullptr && (st = check_ints(first, "first")) != PI_OK) return st;
   if (batch->rows == 0) return ok();
   if ((st = check_rows(k, "k")) != PI_OK || (st = check_rows(v, "v")) != PI_OK) return st;
-  pik::KvStoreArgs a{view_of(h, layer, batch), rows_of(k), rows_of(v), first};
+  pik::KvStoreArgs a{view_of(h, layer, batch), rows_of(k), rows_of(v), first, nullptr};
   return launched(pik::launch_kv_read(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "read");
 }
 

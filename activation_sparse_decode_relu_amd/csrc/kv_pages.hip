@@ -25,7 +25,10 @@ __global__ __launch_bounds__(256) void k_kv_free(const KvPool P, const int* __re
     const int p = atomicExch(row + j, -1);
     if (p >= 0 && p < P.pages) atomicSub(P.refs + p, 1);
   }
-  if (threadIdx.x == 0) P.lens[s] = 0;
+  if (threadIdx.x == 0) {
+    P.lens[s] = 0;
+    P.refused[s] = 0;
+  }
 }
 
 __global__ __launch_bounds__(256) void k_kv_fork(const KvPool P, const int* __restrict__ srcs,
@@ -39,7 +42,10 @@ __global__ __launch_bounds__(256) void k_kv_fork(const KvPool P, const int* __re
     to[j] = p;
     if (p >= 0 && p < P.pages) atomicAdd(P.refs + p, 1);
   }
-  if (threadIdx.x == 0) P.lens[b] = P.lens[a];
+  if (threadIdx.x == 0) {
+    P.lens[b] = P.lens[a];
+    P.refused[b] = P.refused[a];
+  }
 }
 
 // What one sequence of a reserve call needs.
@@ -55,9 +61,9 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   r.shared = -1;
   r.len = r.end = r.have = 0;
   const int c = counts[i];
-  if (r.s < 0 || r.s >= P.max_seqs || c < 0) return r;
+  if (r.s < 0 || r.s >= P.max_seqs) return r;
   r.len = P.lens[r.s];
-  if (r.len < 0) return r;
+  if (r.len < 0 || c < 0) return r;
   const long long end = (long long)r.len + c;
   if (end > (long long)P.max_pages * P.page_tokens) return r;
   r.end = (int)end;
@@ -152,6 +158,8 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
     if (i < n) {
       P.src[i] = from;
       P.dst[i] = to;
+      // see k_kv_append; a request for no tokens says nothing about those of another
+      if (r.s >= 0 && r.s < P.max_seqs && counts[i] > 0) P.refused[r.s] = grows ? 0 : r.len + 1;
     }
     given = min(given + total, P.pages + 1);
   }

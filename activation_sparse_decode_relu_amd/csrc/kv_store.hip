@@ -107,7 +107,9 @@ __global__ __launch_bounds__(2 * D) void k_kv_append(const KvStoreArgs A) {
   const KvSeq s = kv_seq(c, i);
   const int before = s.len - s.rows;                     // tokens held earlier
   const int block = max(before, 0) / kKvBlock + local;
-  if (s.rows == 0 || block * kKvBlock >= s.len) return;
+  // a sequence that reserve refused has no room for these: its last tokens are others, and stay
+  const bool refused = s.seq >= 0 && A.refused[s.seq] == s.len + 1;
+  if (s.rows == 0 || block * kKvBlock >= s.len || refused) return;
   const int page = kv_page(c, s.seq, block);
   if (page < 0) return;
   const size_t at = block_at(c, page, head, block % c.page_blocks);

@@ -16,7 +16,7 @@ from .binding import LIB, PI_ERR_INVALID, PiError, _invalid, check
 PI_KV_F16, PI_KV_BF16 = range(2)
 PI_KV_E4M3, PI_KV_INT8 = range(2)
 KV_BLOCK = 32
-KV_ABI_VERSION = 1   # PI_KV_ABI_VERSION of the header this binding follows
+KV_ABI_VERSION = 2   # PI_KV_ABI_VERSION of the header this binding follows
 
 ACTS = {"f16": PI_KV_F16, "bf16": PI_KV_BF16}
 CODES = {"e4m3": PI_KV_E4M3, "int8": PI_KV_INT8}
@@ -34,7 +34,7 @@ class KvDesc(ctypes.Structure):
 
 
 class KvBuffers(ctypes.Structure):
-    _fields_ = [(name, _vp) for name in ("k", "v", "k_exp", "v_exp", "table", "lens", "refs", "failed")]
+    _fields_ = [(name, _vp) for name in ("k", "v", "k_exp", "v_exp", "table", "lens", "refs", "failed", "refused")]
 
 
 class KvBatch(ctypes.Structure):
@@ -102,6 +102,7 @@ class KVCache:
         lens           int32 [max_seqs]                   tokens of each sequence
         refs           int32 [pages]                      table entries that name a page; 0 = free
         failed         int32 [1]                          sequences that reserve could not grow
+        refused        int32 [max_seqs]                   lens + 1 of each of them until it grows, else 0
 
     `buffers` may bring any of them; the others are made here, empty.  A step of a decode loop is
 
@@ -131,9 +132,10 @@ class KVCache:
         exps = d.kv_heads * (d.page_tokens // KV_BLOCK)
         shapes = dict(k=(d.layers, d.pages, per_page), v=(d.layers, d.pages, per_page),
                       k_exp=(d.layers, d.pages, exps), v_exp=(d.layers, d.pages, exps),
-                      table=(d.max_seqs, d.max_seq_pages), lens=(d.max_seqs,), refs=(d.pages,), failed=(1,))
+                      table=(d.max_seqs, d.max_seq_pages), lens=(d.max_seqs,), refs=(d.pages,), failed=(1,),
+                      refused=(d.max_seqs,))
         for name, shape in shapes.items():
-            dtype = torch.int32 if name in ("table", "lens", "refs", "failed") else torch.uint8
+            dtype = torch.int32 if name in ("table", "lens", "refs", "failed", "refused") else torch.uint8
             t = given.pop(name, None)
             if t is None:
                 if dtype is torch.uint8:
@@ -239,7 +241,8 @@ class KVCache:
     def append(self, layer, k, v, seqs, starts, stream=None) -> None:
         """Store the last tokens of each sequence: rows [starts[i], starts[i + 1]) of k and v
         [rows][kv_heads][head_dim] are the last of the lens[seqs[i]] tokens of seqs[i] (reserve has
-        counted them).  Blocks of 32 tokens and a head share an exponent: see pi_kv.h."""
+        counted them).  A sequence that reserve refused stores nothing.  Blocks of 32 tokens and a head
+        share an exponent: see pi_kv.h."""
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k, "k", heads)
@@ -293,7 +296,7 @@ class KVCache:
     def reserve(self, seqs, counts, stream=None) -> None:
         """Room for counts[i] more tokens of seqs[i], counted in lens: free pages from the lowest number
         up, and a page of its own for a sequence whose partly filled last page is shared.  What does
-        not fit stays as it is and is counted in `failed` (check_failed)."""
+        not fit stays as it is, takes no tokens from append, and is counted in `failed` (check_failed)."""
         n = self._ids(seqs, "seqs")
         self._ids(counts, "counts", n)
         check(LIB.pi_kv_reserve(self._live(), seqs.data_ptr(), counts.data_ptr(), n, self._stream(stream, (seqs, counts))))

@@ -28,8 +28,9 @@
  *     V  token u, dim c  ->  (c / 32) * 1024 + (16 * (u / 8) + c % 16) * 16 + 8 * ((c / 16) % 2) + u % 8
  * - table: int32 [max_seqs][max_seq_pages], the pages of each sequence in order, -1 where there is none.
  *   lens: int32 [max_seqs], tokens of each sequence.  refs: int32 [pages], how many table entries name
- *   each page; a page with 0 is free.  They are the caller's device memory and may be set by the caller
- *   between calls.
+ *   each page; a page with 0 is free.  refused: int32 [max_seqs], lens + 1 of a sequence whose last
+ *   request for tokens pi_kv_reserve could not meet, else 0.  They are the caller's device memory and may
+ *   be set by the caller between calls.
  *
  * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
  * --------------------------------------------------------------------------------------------------
@@ -54,7 +55,7 @@
 extern "C" {
 #endif
 
-#define PI_KV_ABI_VERSION 1
+#define PI_KV_ABI_VERSION 2
 
 #define PI_KV_BLOCK 32 /* tokens that share an exponent */
 
@@ -83,6 +84,7 @@ typedef struct pi_kv_buffers {
   int32_t* lens;
   int32_t* refs;
   int32_t* failed; /* [1]: sequences that pi_kv_reserve could not grow, summed    */
+  int32_t* refused; /* [max_seqs]: which these are, see above                     */
 } pi_kv_buffers;
 
 /* The tokens of one call: see the conventions above. */
@@ -119,8 +121,8 @@ pi_status pi_kv_workspace_bytes(const pi_kv_desc* desc, size_t* bytes);
 
 /*
  * Bind buffers and workspace (256-byte aligned) to a new handle and clear the workspace's counters
- * with a kernel on `stream`.  The buffers' contents are the caller's to set: table -1, lens, refs and
- * failed 0 for an empty cache; codes and exponents need no initial value.
+ * with a kernel on `stream`.  The buffers' contents are the caller's to set: table -1, lens, refs,
+ * failed and refused 0 for an empty cache; codes and exponents need no initial value.
  */
 pi_status pi_kv_create(const pi_kv_desc* desc, const pi_kv_buffers* buffers, void* workspace, size_t workspace_bytes,
                        void* stream, pi_kv** out);
@@ -133,6 +135,11 @@ pi_status pi_kv_destroy(pi_kv* h);
  * count = starts[i + 1] - starts[i].  lens already counts them (pi_kv_reserve), and their pages are in
  * the table.  Other tokens of a block that has them keep their values, up to the rounding that a larger
  * exponent brings; tokens past the sequence's end become zeros.  rows = 0 enqueues nothing.
+ *
+ * Nothing is stored for a sequence that pi_kv_reserve refused at the length it still has (refused[s] =
+ * lens[s] + 1): its last tokens are not those of this call.  So a step that is enqueued as a whole keeps
+ * what is stored, pages shared with other sequences among it; pi_kv_attend then stands at the tokens that
+ * are there, and its rows of that sequence mean nothing.  A reserve that grows it, or a free, ends that.
  */
 pi_status pi_kv_append(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_rows* v, const pi_kv_batch* batch,
                        void* stream);
@@ -160,7 +167,7 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
  * lowest number up, in the order of seqs, and a last page that is partly filled and shared (refs > 1 before
  * the call) is copied, in every layer, to a page of the sequence's own.  A sequence whose table row is
  * too short stays as it is; so do the first for which too few pages are free and all after it.  Each of
- * these is counted in `failed`.
+ * these is counted in `failed` and, unless it asked for 0 tokens, marked in `refused`.
  */
 pi_status pi_kv_reserve(pi_kv* h, const int32_t* seqs, const int32_t* counts, int32_t n, void* stream);
 
