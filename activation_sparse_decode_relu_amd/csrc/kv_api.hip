@@ -23,7 +23,7 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
 struct Layout {
-  size_t tickets, count, src, dst, list, partial, total;
+  size_t tickets, count, src, dst, list, drop, partial, total;
 };
 
 Layout layout_for(const pi_kv_desc& d) {
@@ -35,6 +35,7 @@ Layout layout_for(const pi_kv_desc& d) {
   L.src = off;   off = align_up(off + copies * sizeof(int));
   L.dst = off;   off = align_up(off + copies * sizeof(int));
   L.list = off;  off = align_up(off + (size_t)d.pages * sizeof(int));
+  L.drop = off;  off = align_up(off + (size_t)d.pages * sizeof(int));
   L.partial = off; off = align_up(off + std::max(pik::step_partial_floats(d.head_dim),
                                               pik::tile_partial_floats(d.head_dim)) * sizeof(float));
   L.total = off;
@@ -114,6 +115,7 @@ pik::KvPool pool_of(const pi_kv* h) {
   p.src = reinterpret_cast<int*>(h->ws + h->L.src);
   p.dst = reinterpret_cast<int*>(h->ws + h->L.dst);
   p.list = reinterpret_cast<int*>(h->ws + h->L.list);
+  p.drop = reinterpret_cast<int*>(h->ws + h->L.drop);
   p.count = reinterpret_cast<int*>(h->ws + h->L.count);
   p.page_bytes = (int64_t)h->page_bytes();
   p.exp_bytes = (int)h->exp_bytes();

@@ -52,13 +52,20 @@ __global__ __launch_bounds__(256) void k_kv_fork(const KvPool P, const int* __re
 struct Need {
   int s, len, end, have, pages;   // pages: new ones, a copy's among them; -1: cannot grow
   int shared;                     // the last page, if it has to be copied, else -1
+  bool named;                     // columns past the length name pages: a caller has lowered it
 };
+
+// The page that a column past a sequence's length still names and that no other entry does: it is used again.
+__device__ __forceinline__ bool keeps(const KvPool& P, int page) {
+  return page >= 0 && page < P.pages && P.refs[page] == 1;
+}
 
 __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const int* counts, int i) {
   Need r;
   r.s = seqs[i];
   r.pages = -1;
   r.shared = -1;
+  r.named = false;
   r.len = r.end = r.have = 0;
   const int c = counts[i];
   if (r.s < 0 || r.s >= P.max_seqs) return r;
@@ -68,19 +75,30 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   if (end > (long long)P.max_pages * P.page_tokens) return r;
   r.end = (int)end;
   r.have = (r.len + P.page_tokens - 1) / P.page_tokens;
-  // one more than there are is as good as any number that cannot be had, and keeps the call's sum in 32 bits
-  r.pages = min((r.end + P.page_tokens - 1) / P.page_tokens - r.have, P.pages + 1);
+  const int cols = (r.end + P.page_tokens - 1) / P.page_tokens - r.have;
   if (c > 0 && r.len % P.page_tokens != 0) {
     const int last = P.table[(size_t)r.s * P.max_pages + r.have - 1];
-    if (last < 0 || last >= P.pages) {
-      r.pages = -1;
-      return r;
-    }
-    if (P.refs[last] > 1) {
-      r.shared = last;
-      ++r.pages;
+    if (last < 0 || last >= P.pages) return r;
+    if (P.refs[last] > 1) r.shared = last;
+  }
+  // columns never name more pages than there are; one too many is as good as any number that cannot be had, and
+  // keeps the call's sum in 32 bits
+  r.pages = min(cols, P.pages + 1);
+  if (r.pages <= P.pages) {
+    const int* row = P.table + (size_t)r.s * P.max_pages + r.have;
+    for (int j = 0; j < cols; j += 8) {
+      int p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = j + e < cols ? row[j + e] : -1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (p[e] >= 0) {
+          r.named = true;
+          r.pages -= keeps(P, p[e]) ? 1 : 0;
+        }
     }
   }
+  r.pages += r.shared >= 0 ? 1 : 0;
   return r;
 }
 
@@ -111,15 +129,15 @@ __device__ int list_free(const KvPool& P, int want) {
 
 __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int* __restrict__ seqs,
                                                       const int* __restrict__ counts, int n) {
-  __shared__ int s_failed;
+  __shared__ int s_failed, s_given;
   const int tid = threadIdx.x;
-  if (tid == 0) s_failed = 0;
+  if (tid == 0) s_failed = s_given = 0;
   // how many pages the call wants in all
   int want = 0;
-  Need mine{0, 0, 0, 0, 0, -1};          // of the first kPlan sequences: seldom are there more
+  Need mine{0, 0, 0, 0, 0, -1, false};   // of the first kPlan sequences: seldom are there more
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    const Need r = i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1};
+    const Need r = i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1, false};
     if (base == 0) mine = r;
     int total;
     block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
@@ -129,11 +147,11 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   __threadfence_block();
   __syncthreads();
   // hand them out in order; what a sequence needs is worked out before anything of it changes, and
-  // shared pages keep their counts until all have been looked at
+  // every page keeps its count until all have been looked at
   int given = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1};
+    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1, false};
     int total;
     const int at = given + block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
     const bool grows = i < n && r.pages >= 0 && at + r.pages <= found;
@@ -146,13 +164,15 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
         from = r.shared;
         to = P.list[k++];
         row[r.have - 1] = to;
-        P.refs[to] = 1;
+        P.drop[at] = from;
       }
-      for (; k < at + r.pages; ++k, ++j) {
-        const int p = P.list[k];
-        row[j] = p;
-        P.refs[p] = 1;
+      for (; k < at + r.pages && j < P.max_pages; ++j) {
+        const int old = r.named ? row[j] : -1;
+        if (keeps(P, old)) continue;
+        P.drop[k] = old >= 0 && old < P.pages && P.refs[old] > 1 ? old : -1;
+        row[j] = P.list[k++];
       }
+      atomicMax(&s_given, at + r.pages);
       P.lens[r.s] = r.end;
     }
     if (i < n) {
@@ -165,8 +185,10 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   }
   __threadfence_block();
   __syncthreads();
-  for (int i = tid; i < n; i += kPlan)
-    if (P.src[i] >= 0) atomicSub(P.refs + P.src[i], 1);
+  for (int k = tid; k < s_given; k += kPlan) {   // all up to the last: who comes after one that fails fails too
+    P.refs[P.list[k]] = 1;
+    if (P.drop[k] >= 0) atomicSub(P.refs + P.drop[k], 1);
+  }
   if (tid == 0) {
     *P.count = n;
     if (s_failed != 0) *P.failed += s_failed;

@@ -295,7 +295,8 @@ class KVCache:
 
     def reserve(self, seqs, counts, stream=None) -> None:
         """Room for counts[i] more tokens of seqs[i], counted in lens: free pages from the lowest number
-        up, and a page of its own for a sequence whose partly filled last page is shared.  What does
+        up, and a page of its own for a sequence whose partly filled last page is shared.  A sequence
+        whose length the caller has lowered (guessed tokens that were not taken) uses its pages again.  What does
         not fit stays as it is, takes no tokens from append, and is counted in `failed` (check_failed)."""
         n = self._ids(seqs, "seqs")
         self._ids(counts, "counts", n)

@@ -31,6 +31,9 @@
  *   each page; a page with 0 is free.  refused: int32 [max_seqs], lens + 1 of a sequence whose last
  *   request for tokens pi_kv_reserve could not meet, else 0.  They are the caller's device memory and may
  *   be set by the caller between calls.
+ * - A caller may lower a length (guessed tokens that were not taken).  The pages past it stay the
+ *   sequence's: its next pi_kv_reserve uses them again, pi_kv_free drops them.  A block keeps the exponent
+ *   that its dropped tokens brought.
  *
  * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
  * --------------------------------------------------------------------------------------------------
@@ -165,7 +168,9 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
 /*
  * Make room for counts[i] more tokens of seqs[i] and count them in lens: free pages are taken from the
  * lowest number up, in the order of seqs, and a last page that is partly filled and shared (refs > 1 before
- * the call) is copied, in every layer, to a page of the sequence's own.  A sequence whose table row is
+ * the call) is copied, in every layer, to a page of the sequence's own.  Columns past the length that
+ * still name a page keep it if no other entry names it (refs 1 before the call); a shared one's refs goes
+ * down by one and a free page takes its place.  A sequence whose table row is
  * too short stays as it is; so do the first for which too few pages are free and all after it.  Each of
  * these is counted in `failed` and, unless it asked for 0 tokens, marked in `refused`.
  */

@@ -140,7 +140,9 @@ def kv_reserve(table, lens, refs, seqs, counts, page):
         have, want = -(-lens[s] // page), -(-end // page)
         last = table[s][have - 1] if lens[s] % page else -1
         shared = c > 0 and last >= 0 and refs[last] > 1
-        need = want - have + (1 if shared else 0)
+        # columns past the length that still name a page: its own stays, a shared one is let go
+        fill = [j for j in range(have, want) if table[s][j] < 0 or refs[table[s][j]] != 1]
+        need = len(fill) + (1 if shared else 0)
         if full or taken + need > len(free):
             full = True
             failed += 1
@@ -151,8 +153,10 @@ def kv_reserve(table, lens, refs, seqs, counts, page):
             copies.append((last, mine[0]))
             dropped.append(last)
             table[s][have - 1] = mine.pop(0)
-        for j, p in enumerate(mine):
-            table[s][have + j] = p
+        for j, p in zip(fill, mine):
+            if table[s][j] >= 0 and refs[table[s][j]] > 1:
+                dropped.append(table[s][j])
+            table[s][j] = p
         lens[s] = end
     for p in free[:taken]:
         refs[p] = 1

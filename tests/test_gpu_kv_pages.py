@@ -156,3 +156,124 @@ def test_a_request_for_no_tokens_is_no_refusal():
     c.reserve(_ids([0]), _ids([0]))
     c.append(0, x[40:], x[40:], _ids([0]), _ids([0, 1]))
     assert np.array_equal(_read_all(c, 0, 0, 40)[0].double().cpu().numpy(), m.values)
+
+
+# ---- lengths that the caller lowers ----------------------------------------------------------------------
+
+
+def _counts_hold(model):
+    table, _, refs = model
+    named = [0] * len(refs)
+    for row in table:
+        for p in row:
+            if p >= 0:
+                named[p] += 1
+    return named == refs
+
+
+def test_pages_past_a_lowered_length_are_used_again():
+    """Guessed tokens that were not taken: their pages stay with the sequence and none is lost."""
+    announce("kv reserve after a rollback")
+    c = _cache(8)
+    model = _state(c)
+    _reserve(c, model, [0, 1], [34, 70], 32)
+    for new_len in (31, 0, 34, 1):
+        c.lens[0] = new_len
+        model[1][0] = new_len
+        _reserve(c, model, [0], [36 - new_len], 32)
+        assert _counts_hold(model) and sum(r > 0 for r in model[2]) == 5
+    c.lens[1] = 64
+    model[1][1] = 64
+    _reserve(c, model, [1, 0], [1, 60], 32)                        # 65 tokens on the page it has; 96 take one more
+    assert sum(r > 0 for r in model[2]) == 6
+    oracle.kv_free(*model, [0, 1])
+    c.free(_ids([0, 1]))
+    assert _state(c) == model and not any(model[2])
+
+
+def test_a_shared_page_past_a_lowered_length_is_let_go():
+    announce("kv reserve after a rollback of forks")
+    c = _cache(9)
+    model = _state(c)
+    _reserve(c, model, [0], [70], 32)
+    oracle.kv_fork(*model, [0, 0], [1, 2])
+    c.fork(_ids([0, 0]), _ids([1, 2]))
+    for s, n in ((0, 32), (1, 40), (2, 20)):
+        c.lens[s] = n
+        model[1][s] = n
+    _reserve(c, model, [0, 1, 2], [40, 1, 0], 32)                  # 0: two pages anew; 1: a copy; 2: nothing
+    assert _counts_hold(model)
+    _reserve(c, model, [1, 2], [30, 80], 32)
+    assert _counts_hold(model)
+    oracle.kv_free(*model, [0, 1, 2])
+    c.free(_ids([0, 1, 2]))
+    assert _state(c) == model and not any(model[2])
+
+
+def test_a_page_that_is_named_but_free_is_anyones():
+    """A caller that has given a page back by its count alone: the entry is replaced, whoever gets the page."""
+    announce("kv reserve, an entry past the length that names a free page")
+    c = _cache(6)
+    model = _state(c)
+    _reserve(c, model, [0, 1], [70, 32], 32)                       # 0, 1, 2 and 3
+    for t, part in ((c.lens, model[1]), (c.refs, model[2])):
+        at, value = (0, 32) if t is c.lens else (1, 0)             # page 1 is in column 1 of sequence 0
+        t[at] = value
+        part[at] = value
+    _reserve(c, model, [1, 0], [1, 40], 32)                        # 1 takes page 1; 0 takes 4 and keeps 2
+    assert model[0][0][:3] == [0, 4, 2] and model[0][1][:2] == [3, 1] and _counts_hold(model)
+
+
+def test_rollbacks_over_a_long_use():
+    """Random reserves, rollbacks, forks, frees and compactions: table, lengths and counts as the oracle's, and every count
+    the number of entries that name the page."""
+    announce("kv pages, random use with rollbacks")
+    rng = np.random.default_rng(31)
+    for page, pages in ((32, 30), (96, 18)):
+        c = _cache(pages, page, seqs=8, width=6)
+        model = _state(c)
+        table, lens, refs = model
+        for step in range(120):
+            kind, some = rng.integers(0, 7), rng.permutation(8)[:rng.integers(1, 6)].tolist()
+            if kind <= 2:
+                _reserve(c, model, some, [int(x) for x in rng.choice([0, 1, 1, 5, page, 70, 200], len(some))], page)
+            elif kind == 3:
+                for s in some:
+                    lens[s] = int(rng.integers(0, lens[s] + 1))
+                c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+            elif kind == 4:
+                oracle.kv_free(*model, some[:2])
+                c.free(_ids(some[:2]))
+            elif kind == 5:
+                dst = [s for s in range(8) if all(p < 0 for p in table[s])][:3]
+                live = [s for s in range(8) if lens[s] > 0]
+                if not dst or not live:
+                    continue
+                src = [live[int(rng.integers(len(live)))] for _ in dst]
+                oracle.kv_fork(*model, src, dst)
+                c.fork(_ids(src), _ids(dst))
+            else:
+                oracle.kv_compact(table, refs)
+                c.compact()
+            assert _state(c) == model and _counts_hold(model), f"step {step}"
+
+
+def test_tokens_after_a_rollback():
+    """What is stored after a rollback: the kept tokens, and new ones on the pages that were kept."""
+    announce("kv append after a rollback")
+    c = _cache(4)
+    x = torch.randn(90, 1, 64, device="cuda").half().clamp(-2, 2)
+    c.reserve(_ids([0]), _ids([70]))
+    c.append(0, x[:70], -x[:70], _ids([0]), _ids([0, 70]))
+    c.lens[0] = 30                                                 # inside a block of 32
+    c.reserve(_ids([0]), _ids([40]))
+    c.append(0, x[50:], -x[50:], _ids([0]), _ids([0, 40]))
+    got = torch.empty(2, 70, 1, 64, dtype=torch.float16, device="cuda")
+    c.read(0, got[0], got[1], _ids([0]), _ids([0, 70]))
+    want = torch.cat([x[:30], x[50:]])
+    # a block keeps the exponent that dropped tokens brought, -7 at most for amax <= 2: a value is off by half a step of e4m3,
+    # 2^-4 of it, or by 2^-10 2^-7 below the normal range, where a larger exponent may round it a second time
+    for t, sign in ((got[0], 1), (got[1], -1)):
+        err = (t.double() - sign * want.double()).abs()
+        assert bool((err <= 2.0 ** -4 * want.double().abs() + 2.0 ** -16).all())
+    assert int((c.refs > 0).sum()) == 3
