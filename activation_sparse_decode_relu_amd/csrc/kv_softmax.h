@@ -82,6 +82,13 @@ __device__ __forceinline__ float out_half(const RowState& s) {
   return s.l > 0.0f ? ex2(0.5f * (s.rr - kBias - s.mm)) : 0.0f;
 }
 __device__ __forceinline__ float out_value(float o, float l, float half) { return l != 0.0f ? o / l * half * half : 0.0f; }
+// A row's value as it is returned: within the type's finite range, as stored values are read (the codes of the largest
+// values stand for the next power of two).  A NaN, which only a query can bring, stays.
+template <int ACT>
+__device__ __forceinline__ typename ActT<ACT>::T rounded(float x) {
+  constexpr float kMax = ActT<ACT>::kMax;
+  return (typename ActT<ACT>::T)(x > kMax ? kMax : x < -kMax ? -kMax : x);
+}
 __device__ __forceinline__ float row_lse(const RowState& s) {
   return s.l > 0.0f ? (s.mm + log2f(s.l)) * kLn2 : (s.l == s.l ? -INFINITY : s.l);
 }

@@ -380,7 +380,7 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
       typedef T T4 __attribute__((ext_vector_type(4)));
       T4 y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = (T)out_value(v[e], a.l, half);
+      for (int e = 0; e < 4; ++e) y[e] = rounded<ACT>(out_value(v[e], a.l, half));
       *reinterpret_cast<T4*>(out) = y;
       if (d == 0 && A.lse != nullptr) A.lse[(size_t)(row0 + j) * A.heads + h] = row_lse(a);
     };

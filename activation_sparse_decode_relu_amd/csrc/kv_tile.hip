@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const KvAttendArgs 
       typedef T T4 __attribute__((ext_vector_type(4)));
       T4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (T)(st.l != 0.0f ? o[d][4 * a + e] * inv * half * half : 0.0f);
+      for (int e = 0; e < 4; ++e) v[e] = rounded<ACT>(st.l != 0.0f ? o[d][4 * a + e] * inv * half * half : 0.0f);
       *reinterpret_cast<T4*>(out + 32 * d + 8 * a + 4 * h) = v;
     }
   if (h == 0 && A.lse != nullptr) A.lse[(size_t)(job.s.row0 + j) * A.heads + hq] = row_lse(st);
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(kTileThreads) void k_kv_tile_join(const KvAttendArg
   const float half = out_half(a);
   T4 w;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) w[e] = (T)out_value(v[e], a.l, half);
+  for (int e = 0; e < 4; ++e) w[e] = rounded<ACT>(out_value(v[e], a.l, half));
   *reinterpret_cast<T4*>(out) = w;
   if (d == 0 && A.lse != nullptr) A.lse[(size_t)(job.s.row0 + j) * A.heads + hq] = row_lse(a);
 }

@@ -161,7 +161,8 @@ pi_status pi_kv_read(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_r
  * u > p - window or u < sinks (all u <= p where window is 0).  With x_u = scale * <q, K_u>:
  *   lse = log sum_u exp(x_u)     out = sum_u exp(x_u - lse) V_u
  * in fp32 (the products of the matrix instructions take exp() rounded to fp16, see the kernels), out
- * rounded once.  A row that sees no token gets out 0 and lse -inf.
+ * clamped to the finite range of the activations' type and rounded once.  A row that sees no token gets
+ * out 0 and lse -inf.
  */
 pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_batch* batch, void* stream);
 

@@ -18,3 +18,32 @@ torch = pytest.importorskip("torch")
 def _need_gpu():
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
+
+
+# ---- values at the ends of their types -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("heads", [(2, 2, 64), (8, 1, 128)])
+def test_the_largest_values_give_finite_outputs(act, code, heads):
+    """The type's largest value is stored as the next power of two, past the type: outputs are held to its finite
+    range, as read's are.  A mean of one value is that value, up to 2^-10 of it, and rounds or is held to the same number."""
+    announce(f"kv attend, largest values {act} {code} {heads}")
+    top = torch.finfo(DT[act]).max
+    n = 700
+    r = Rig([n, 40], *heads, 64, act, code, seed=50)
+    v = [r.tokens(c, heads[1], 0.5) for c in (n, 40)]
+    v = torch.cat(v)
+    v[:, :, 3], v[:, :, 17] = top, -top
+    v[:, :, 40] = float("inf")
+    r.append([n, 40], v=v)
+    r.check_stored()
+    for counts in ([1, 1], [6, 3], [130, 40]):
+        total = sum(counts)
+        q = r.tokens(total, heads[0]).cuda()
+        out = torch.full((total, heads[0], heads[2]), float("nan"), dtype=DT[act], device="cuda")
+        starts = _ids([0, counts[0], total])
+        r.cache.attend(0, q, out, _ids([0, 1]), starts, max(counts))
+        assert bool(torch.isfinite(out).all())
+        assert bool((out[:, :, 3] == top).all()) and bool((out[:, :, 17] == -top).all()) and bool((out[:, :, 40] == top).all())
