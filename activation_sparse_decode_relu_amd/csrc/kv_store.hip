@@ -195,11 +195,12 @@ __global__ __launch_bounds__(2 * D) void k_kv_read(const KvStoreArgs A) {
   const int i = slot_owner(c, blockIdx.x / c.kv_heads, 1, kKvBlock, 2, local);
   const KvSeq s = kv_seq(c, i);
   const int first = A.first != nullptr ? min(A.first[i], 1 << 30) : 0;   // past any sequence's end all is 0
-  // blocks are counted from the one that holds token `first`; tokens below 0 have no block
-  const int lo = max(first, 0), block = lo / kKvBlock + local;
+  // blocks are counted from the one that holds token `first`, below token 0 too: what is not there reads as 0
+  const int block = (first >> 5) + local;
+  static_assert(kKvBlock == 1 << 5, "rounds down");
   const long long end = (long long)first + s.rows;      // past the last token asked for
   if (s.rows == 0 || (long long)block * kKvBlock >= end) return;
-  const int page = block * kKvBlock < s.len ? kv_page(c, s.seq, block) : -1;
+  const int page = block >= 0 && block * kKvBlock < s.len ? kv_page(c, s.seq, block) : -1;
   const size_t at = page >= 0 ? block_at(c, page, head, block % c.page_blocks) : 0;
   const Place<D> my_place(tid);
   float fk = 0.0f, fv = 0.0f;

@@ -254,7 +254,7 @@ class KVCache:
 
     def read(self, layer, k_out, v_out, seqs, starts, first=None, stream=None) -> None:
         """Read tokens back: rows [starts[i], starts[i + 1]) of k_out and v_out get the tokens of seqs[i]
-        from first[i] on (from 0 where first is None); tokens past the end read as 0."""
+        from first[i] on (from 0 where first is None); tokens past the end or before the first read as 0."""
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k_out, "k_out", heads)

@@ -150,7 +150,7 @@ pi_status pi_kv_append(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv
 /*
  * Read tokens back: row starts[i] + j gets token first[i] + j of seqs[i] (first NULL: from token 0), as
  * code * 2^e clamped to the finite range of the activations' type and rounded to it once.  Tokens past
- * the end, or of no page, read as 0.
+ * the end, before token 0, or of no page, read as 0.
  */
 pi_status pi_kv_read(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_rows* v, const pi_kv_batch* batch,
                      const int32_t* first, void* stream);

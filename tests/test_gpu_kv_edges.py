@@ -47,3 +47,23 @@ def test_the_largest_values_give_finite_outputs(act, code, heads):
         r.cache.attend(0, q, out, _ids([0, 1]), starts, max(counts))
         assert bool(torch.isfinite(out).all())
         assert bool((out[:, :, 3] == top).all()) and bool((out[:, :, 17] == -top).all()) and bool((out[:, :, 40] == top).all())
+
+
+# ---- states that only the device knows -------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("first", [-1, -31, -32, -33, -70, -(1 << 31), (1 << 31) - 1])
+def test_read_from_before_the_first_token(first):
+    """Tokens before the first are not there: they read as 0, and no row is left out."""
+    announce(f"kv read from {first}")
+    r = Rig([100, 70], 2, 2, 64, 32, seed=51)
+    r.append([100, 70])
+    got = [torch.full((140, 2, 64), 7.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    r.cache.read(0, got[0], got[1], _ids([1, 0]), _ids([0, 75, 140]), first=_ids([first, 95]))
+    for t, models in ((got[0], r.k), (got[1], r.v)):
+        want = np.zeros((140, 2, 64))
+        for row in range(75):
+            if 0 <= first + row < 70:
+                want[row] = models[1].values[first + row]
+        want[75:80] = models[0].values[95:100]
+        assert np.array_equal(_f64(t), want)
