@@ -99,7 +99,7 @@ __device__ __forceinline__ size_t block_at(const KvView& c, int page, int head, 
 // One sequence of a call.
 struct KvSeq {
   int seq;     // row of the table, -1 if out of range
-  int len;     // tokens it holds
+  int len;     // tokens it holds; 0 if the length is out of range
   int row0;    // its first row
   int rows;    // its rows
 };
@@ -109,7 +109,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvView& c, int i) {
   const int r0 = min(max(c.starts[i], 0), c.rows), r1 = min(c.starts[i + 1], c.rows);
   const int q = c.seqs[i];
   s.seq = q >= 0 && q < c.max_seqs ? q : -1;
-  s.len = s.seq >= 0 ? min(max(c.lens[q], 0), c.max_pages * c.page_blocks * kKvBlock) : 0;
+  const int len = s.seq >= 0 ? c.lens[q] : 0;
+  s.len = len >= 0 && len <= c.max_pages * c.page_blocks * kKvBlock ? len : 0;
   s.row0 = r0;
   s.rows = max(r1 - r0, 0);
   return s;

@@ -67,3 +67,28 @@ def test_read_from_before_the_first_token(first):
                 want[row] = models[1].values[first + row]
         want[75:80] = models[0].values[95:100]
         assert np.array_equal(_f64(t), want)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), 129, 1 << 20, (1 << 31) - 1])
+def test_a_length_out_of_range_is_no_length(length):
+    """Lengths below 0 or past the table's columns (4 pages of 32 here) read as nothing and write nothing."""
+    announce(f"kv, a length of {length}")
+    r = Rig([70, 90], 8, 2, 64, 32, seed=52)
+    r.append([70, 90])
+    assert r.cache.table.shape[1] * 32 == 128
+    r.cache.table[0] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)   # pages in every column, whosever they are
+    r.cache.lens[0] = length
+    bytes_before = [getattr(r.cache, n).clone() for n in ("k", "v", "k_exp", "v_exp")]
+    t = r.tokens(3, 2).cuda()
+    r.cache.append(0, t, t, _ids([0]), _ids([0, 3]))
+    for n, old in zip(("k", "v", "k_exp", "v_exp"), bytes_before):
+        assert torch.equal(getattr(r.cache, n), old), n
+    got = [torch.full((128, 2, 64), 7.0, dtype=torch.float16, device="cuda") for _ in range(2)]
+    r.cache.read(0, got[0], got[1], _ids([0]), _ids([0, 128]))
+    assert not bool(got[0].any()) and not bool(got[1].any())
+    for rows in (2, 40):
+        q = r.tokens(rows, 8).cuda()
+        out = torch.full((rows, 8, 64), float("nan"), dtype=torch.float16, device="cuda")
+        lse = torch.zeros(rows, 8, device="cuda")
+        r.cache.attend(0, q, out, _ids([0]), _ids([0, rows]), rows, lse=lse)
+        assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
