@@ -8,11 +8,12 @@
 // rr follows the largest x_u + ev seen, so w stays in fp16's range whatever the exponents are, and the
 // softmax's own sum takes the factor back once for a block:
 //     l = sum_blocks 2^(rr - kBias - ev - mm) sum_u w_u,     mm near the largest x_u.
-// Both references only move when a block passes them by more than kSlack, and l by more than kFar, so most
+// Both references only move when a block passes rr by more than kSlack or mm by more than kLead, so most
 // blocks rescale nothing; w is then at most 2^(kBias + kSlack) = 2^15.  (With slack 5 and bias 10, 32 rows of
 // scores with a deviation of 3 found one that moves in every other tile: a prompt of 4096 took 335 us
-// instead of 324.)  A block whose V is more than 2^kFar smaller than the row's largest product is taken as
-// 2^kFar smaller: it cannot show in O (fp32), and its w, which l needs, cannot underflow.  w is rounded to fp16,
+// instead of 324.)  A block whose V is so small that its tokens with x_u = mm lie more than 2^kFar below the row's
+// largest product is taken as 2^kFar below, so that its w, which l needs, cannot underflow.  In O it cannot show: with
+// x_u <= mm + kLead its w is at most 2^(kBias + kLead - kFar) = 2^-35, which is zero in fp16.  w is rounded to fp16,
 // half a step of 2^-11, or 2^-25 / 2^kBias = 2^-30 of the row's largest where that is more; everything else is fp32.
 #pragma once
 
@@ -20,7 +21,7 @@
 
 namespace pik {
 
-constexpr float kBias = 5.0f, kSlack = 10.0f, kFar = 60.0f;
+constexpr float kBias = 5.0f, kSlack = 10.0f, kLead = 20.0f, kFar = 60.0f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -45,7 +46,7 @@ __device__ __forceinline__ float score_factor(float row, int ek) {
 
 // Does this lane's largest score of the block, `top` (already scaled), pass the references?
 __device__ __forceinline__ bool passes(const RowState& s, float top, float ev) {
-  return top + ev > s.rr + kSlack || top > s.mm + kFar;
+  return top + ev > s.rr + kSlack || top > s.mm + kLead;
 }
 
 // New references from the row's largest score of the block (the same in all of the row's lanes);

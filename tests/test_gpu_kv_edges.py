@@ -92,3 +92,35 @@ def test_a_length_out_of_range_is_no_length(length):
         lse = torch.zeros(rows, 8, device="cuda")
         r.cache.attend(0, q, out, _ids([0]), _ids([0, rows]), rows, lse=lse)
         assert bool((out == 0).all()) and bool((lse == -float("inf")).all())
+
+
+# ---- blocks of V far smaller than others -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("nats", [16, 24, 32, 40, 48])
+@pytest.mark.parametrize("heads, rows", [((4, 1, 64), 1), ((8, 1, 64), 7), ((8, 1, 64), 9), ((2, 2, 128), 70)])
+def test_a_tiny_block_with_a_large_score(code, nats, heads, rows):
+    """One token's V is 1 and its score 0; a later block's V is 2^-100 and one of its scores `nats`.  The output is the
+    first token's share, e^-nats, far above what the tiny block adds.  Bound: that of test_gpu_kv, its floor 2^-30 a token of
+    the row's own largest term (never more than mass)."""
+    announce(f"kv attend, tiny block {code} {nats} {heads} {rows}")
+    n = 160 + rows
+    r = Rig([n], *heads, 64, "bf16", code, seed=53)
+    k, v = torch.zeros(n, heads[1], heads[2]), torch.zeros(n, heads[1], heads[2])
+    v[0] = 1.0
+    v[128:160] = 2.0 ** -100
+    k[130, :, 0] = nats                                # exact in both codes
+    r.append([n], k=k.bfloat16(), v=v.bfloat16())
+    r.check_stored()
+    q = torch.zeros(rows, heads[0], heads[2])
+    q[..., 0] = 1.0
+    q = q.bfloat16()
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(rows, heads[0], device="cuda")
+    r.cache.attend(0, q.cuda(), out, _ids([0]), _ids([0, rows]), rows, scale=1.0, lse=lse)
+    ref, ref_lse, mass, reach = oracle.kv_attend(_f64(q), r.k[0].values, r.v[0].values, scale=1.0)
+    dx = reach * ((heads[2] + 4) * 2.0 ** -24 + 2.0 ** -23)
+    rel = np.expm1(2 * dx) + (n + 16) * 2.0 ** -24 + 2.0 ** -11 + n * 2.0 ** -30
+    assert np.all(np.abs(_f64(out) - ref) <= rel[..., None] * mass + EPS["bf16"] * np.abs(ref))
+    assert np.all(np.abs(_f64(lse) - ref_lse) <= dx + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(ref_lse)))
