@@ -271,16 +271,14 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
   // there are items enough: eight tokens on one head of eight query heads, sequences of 4000, took 34.9 us against
   // 24.1 through LDS with 16 items, 36.4 against 31.1 with 32, 41.2 against 41.8 with 64 and 56 against 82 with 128.
   // With 64 dims, four tokens of 16 query heads, 48.6 against 62.7 us over 100003 tokens, 18.1 against 14.2 over 2000.
+  // That kernel counts the call's blocks of 32 tokens in 32 bits: a table with room for more (2^30 tokens each of eight
+  // sequences on eight heads, say) goes through LDS, whatever it holds.
   const int64_t shared = (int64_t)a.max_new * a.group, items = (int64_t)a.c.n * a.c.kv_heads;
-  if (shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32)) {
-    // the kernel counts the call's blocks of 32 tokens in 32 bits
-    const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
-    const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + a.max_new) / PI_KV_BLOCK + 4) : cap;
-    if ((seen + pik::kStepGrain) * a.c.kv_heads * a.c.n > INT32_MAX)
-      return fail(PI_ERR_UNSUPPORTED, "%d sequences of up to %lld blocks and %d heads are more than one call takes", a.c.n,
-                  (long long)seen, a.c.kv_heads);
+  const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
+  const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + a.max_new) / PI_KV_BLOCK + 4) : cap;
+  const bool counts = (seen + pik::kStepGrain) * items <= INT32_MAX;
+  if (counts && shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32))
     return launched(pik::launch_kv_step(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
-  }
   return launched(pik::launch_kv_tile(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
 }
 

@@ -124,3 +124,22 @@ def test_a_tiny_block_with_a_large_score(code, nats, heads, rows):
     rel = np.expm1(2 * dx) + (n + 16) * 2.0 ** -24 + 2.0 ** -11 + n * 2.0 ** -30
     assert np.all(np.abs(_f64(out) - ref) <= rel[..., None] * mass + EPS["bf16"] * np.abs(ref))
     assert np.all(np.abs(_f64(lse) - ref_lse) <= dx + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(ref_lse)))
+
+
+# ---- what a table may hold, and what it holds ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("window, sinks", [(0, 0), (50, 2), ((1 << 31) - 1, (1 << 31) - 1)])
+def test_a_table_far_larger_than_its_sequences(window, sinks):
+    """9 sequences on 8 cached heads with room for 2^30 tokens each: what they hold decides, not what the table could."""
+    import activation_sparse_decode_relu_amd as pi
+    announce(f"kv attend, a table of 2^30 tokens, window {window}")
+    lens = [1, 5000, 33, 64, 100, 7, 300, 31, 4097]
+    r = Rig(lens, 8, 8, 64, 4096, seed=54)
+    own = {name: getattr(r.cache, name) for name in ("k", "v", "k_exp", "v_exp", "lens", "refs")}
+    narrow = r.cache.table
+    r.cache = pi.KVCache(8, 8, 64, r.cache.desc.pages, 4096, len(lens), 1 << 18, buffers=own)
+    r.cache.table[:, :narrow.shape[1]] = narrow
+    r.append(lens)
+    r.attend([1] * 9, window, sinks)
+    r.attend([1, 5, 0, 2, 1, 1, 70, 3, 1], window, sinks)
