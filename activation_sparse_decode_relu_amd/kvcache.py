@@ -76,12 +76,20 @@ _declare()
 _byref = ctypes.byref
 
 
+def _in32(value, name):
+    """A number that the C ABI takes in 32 bits: ctypes would cut one that does not fit."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise _invalid(f"{name}={value} does not fit in 32 bits")
+    return value
+
+
 def kv_desc(heads, kv_heads, head_dim, pages, page_tokens, max_seqs, max_seq_pages, layers=1, act_dtype="f16",
             code="e4m3") -> KvDesc:
     act = ACTS[act_dtype] if isinstance(act_dtype, str) else int(act_dtype)
     c = CODES[code] if isinstance(code, str) else int(code)
-    return KvDesc(int(heads), int(kv_heads), int(head_dim), int(page_tokens), int(pages), int(layers), int(max_seqs),
-                  int(max_seq_pages), act, c)
+    sizes = dict(heads=heads, kv_heads=kv_heads, head_dim=head_dim, page_tokens=page_tokens, pages=pages, layers=layers,
+                 max_seqs=max_seqs, max_seq_pages=max_seq_pages, act_dtype=act, code=c)
+    return KvDesc(*[_in32(int(value), name) for name, value in sizes.items()])
 
 
 def kv_workspace_bytes(desc: KvDesc) -> int:
@@ -243,18 +251,20 @@ class KVCache:
         [rows][kv_heads][head_dim] are the last of the lens[seqs[i]] tokens of seqs[i] (reserve has
         counted them).  A sequence that reserve refused stores nothing.  Blocks of 32 tokens and a head
         share an exponent: see pi_kv.h."""
+        layer = _in32(layer, "layer")
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k, "k", heads)
         rows = k.shape[0]
         vr = self._rows(v, "v", heads, rows)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
         check(LIB.pi_kv_append(self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
                                self._stream(stream, (k, v, seqs, starts))))
 
     def read(self, layer, k_out, v_out, seqs, starts, first=None, stream=None) -> None:
         """Read tokens back: rows [starts[i], starts[i + 1]) of k_out and v_out get the tokens of seqs[i]
         from first[i] on (from 0 where first is None); tokens past the end or before the first read as 0."""
+        layer = _in32(layer, "layer")
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k_out, "k_out", heads)
@@ -264,7 +274,7 @@ class KVCache:
         self._writable(v_out, "v_out")
         if first is not None:
             self._ids(first, "first", n)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
         check(LIB.pi_kv_read(self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
                              None if first is None else first.data_ptr(),
                              self._stream(stream, (k_out, v_out, seqs, starts, first))))
@@ -277,6 +287,7 @@ class KVCache:
         denominator.  max_new: at least the largest count of rows of a sequence (rows past it are not
         computed).  scale: head_dim ** -0.5 unless given."""
         d = self.desc
+        layer = _in32(layer, "layer")
         n = self._ids(seqs, "seqs")
         self._ids(starts, "starts", n + 1)
         qr = self._rows(q, "q", d.heads)
@@ -285,9 +296,10 @@ class KVCache:
         self._writable(out, "out")
         if lse is not None:
             self._dense(lse, "lse", torch.float32, (rows, d.heads))
-        args = KvAttendArgs(qr, orow, None if lse is None else lse.data_ptr(), max_new, window, sinks,
+        args = KvAttendArgs(qr, orow, None if lse is None else lse.data_ptr(), _in32(max_new, "max_new"),
+                            _in32(window, "window"), _in32(sinks, "sinks"),
                             d.head_dim ** -0.5 if scale is None else scale)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
         check(LIB.pi_kv_attend(self._live(), layer, _byref(args), _byref(batch),
                                self._stream(stream, (q, out, seqs, starts, lse))))
 
