@@ -37,6 +37,9 @@ class KvBuffers(ctypes.Structure):
     _fields_ = [(name, _vp) for name in ("k", "v", "k_exp", "v_exp", "table", "lens", "refs", "failed", "refused")]
 
 
+_OWNED = tuple(name for name, _ in KvBuffers._fields_) + ("workspace",)   # a cache's tensors
+
+
 class KvBatch(ctypes.Structure):
     _fields_ = [("seqs", _vp), ("starts", _vp), ("n", _i32), ("rows", _i32)]
 
@@ -159,6 +162,7 @@ class KVCache:
         if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
             raise _invalid(f"workspace must be a contiguous tensor on {device}")
         self.workspace = workspace
+        self._met = set()
         if device.type != "cuda":
             raise _invalid(f"the cache must be on a CUDA device, not {device}")
         self._act = _ACT_TORCH[d.act_dtype]
@@ -232,12 +236,21 @@ class KVCache:
             raise _invalid(f"{name}: its rows overlap")
 
     def _stream(self, stream, tensors) -> int:
+        """The stream's handle.  Memory that is let go of stays reserved until the stream is past the call: the given
+        tensors where the caller names a stream (the current one is theirs to mind, as everywhere in torch), and, once for
+        each stream that the cache meets, the cache's own."""
         if stream is None:
-            return torch.cuda.current_stream(self.device.index).cuda_stream or None
-        for t in tensors:   # memory the caller lets go of stays theirs until this stream is past the call
-            if t is not None:
-                t.record_stream(stream)
-        return stream.cuda_stream or None
+            stream = torch.cuda.current_stream(self.device.index)
+        else:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        handle = stream.cuda_stream
+        if handle not in self._met:
+            self._met.add(handle)
+            for name in _OWNED:
+                getattr(self, name).record_stream(stream)
+        return handle or None
 
     def _live(self):
         if self.handle is None:

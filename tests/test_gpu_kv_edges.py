@@ -143,3 +143,36 @@ def test_a_table_far_larger_than_its_sequences(window, sinks):
     r.append(lens)
     r.attend([1] * 9, window, sinks)
     r.attend([1, 5, 0, 2, 1, 1, 70, 3, 1], window, sinks)
+
+
+# ---- streams ---------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("named", [True, False])
+def test_a_cache_dropped_while_another_stream_works(named):
+    """The pages stay reserved until that stream is past its calls, whether it is named or is the current one."""
+    import activation_sparse_decode_relu_amd as pi
+    announce("kv, a cache dropped early")
+    side = torch.cuda.Stream()
+    c = pi.KVCache(4, 4, 64, 400, 32, 4, 100)
+    ids, counts = _ids(range(4)), _ids([3000] * 4)
+    c.reserve(ids, counts)
+    size = c.k.numel()
+    x = torch.randn(12000, 4, 64, device="cuda").half()
+    starts = _ids(range(0, 12001, 3000))
+    c.append(0, x, x, ids, starts)
+    q, one = torch.randn(4, 4, 64, device="cuda").half(), _ids(range(5))
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    c.attend(0, q, want, ids, one, 1)
+    torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)                   # cycles: some 25 ms before the call's turn
+        if not named:
+            c.attend(0, q, got, ids, one, 1)
+    if named:
+        c.attend(0, q, got, ids, one, 1, stream=side)
+    del c
+    torch.full((size,), 255, dtype=torch.uint8, device="cuda")   # takes any memory of that size that is free
+    side.synchronize()
+    assert torch.equal(got, want)

@@ -26,3 +26,32 @@ def test_numbers_past_32_bits_are_refused(value):
         _rejects(lambda: pi.kv_desc(**{**GOOD, name: value}), name)
     for name in ("act_dtype", "code"):
         _rejects(lambda: pi.kv_desc(**GOOD, **{name: value}), name)
+
+
+OWNED = ("k", "v", "k_exp", "v_exp", "table", "lens", "refs", "failed", "refused", "workspace")
+
+
+class _Memory:
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def test_a_stream_holds_the_caches_own_memory():
+    """A cache that is dropped while a stream still works on it keeps its memory until that stream is past its calls."""
+    c, side, other = _cache(), SimpleNamespace(cuda_stream=5), SimpleNamespace(cuda_stream=9)
+    c._met, mine = set(), {name: _Memory() for name in OWNED}
+    for name, m in mine.items():
+        setattr(c, name, m)
+    arg = _Memory()
+    assert c._stream(side, (arg, None)) == 5
+    assert arg.streams == [side]
+    for name, m in mine.items():
+        assert m.streams == [side], name
+    c._stream(other, ())
+    c._stream(side, (arg,))
+    assert arg.streams == [side, side]                  # another call's tensor, as far as the cache knows
+    for name, m in mine.items():
+        assert m.streams[:2] == [side, other], name
