@@ -166,6 +166,8 @@ class KVCache:
         if device.type != "cuda":
             raise _invalid(f"the cache must be on a CUDA device, not {device}")
         self._act = _ACT_TORCH[d.act_dtype]
+        if stream is not None:   # it is the buffers' first user, and they were filled on the current one
+            stream.wait_stream(torch.cuda.current_stream(device.index))
         handle = _vp()
         buf = KvBuffers(*[getattr(self, name).data_ptr() for name, _ in KvBuffers._fields_])
         check(LIB.pi_kv_create(_byref(d), _byref(buf), workspace.data_ptr(),

@@ -176,3 +176,19 @@ def test_a_cache_dropped_while_another_stream_works(named):
     torch.full((size,), 255, dtype=torch.uint8, device="cuda")   # takes any memory of that size that is free
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_cache_made_on_a_stream_is_empty_there():
+    """The buffers a cache makes for itself are set before the given stream's first call, however late the current one is."""
+    import activation_sparse_decode_relu_amd as pi
+    announce("kv create on another stream")
+    side = torch.cuda.Stream()
+    ids, counts = _ids([0, 2]), _ids([40, 33])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                      # cycles: some 50 ms before the current stream gets to the fills
+    c = pi.KVCache(2, 1, 64, 6, 32, 3, 4, stream=side)
+    c.reserve(ids, counts, stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert c.lens.tolist() == [40, 0, 33] and c.refs.tolist() == [1, 1, 1, 1, 0, 0]
+    assert c.table.tolist() == [[0, 1, -1, -1], [-1] * 4, [2, 3, -1, -1]] and int(c.failed.item()) == 0
