@@ -192,3 +192,59 @@ def test_a_cache_made_on_a_stream_is_empty_there():
     torch.cuda.synchronize()
     assert c.lens.tolist() == [40, 0, 33] and c.refs.tolist() == [1, 1, 1, 1, 0, 0]
     assert c.table.tolist() == [[0, 1, -1, -1], [-1] * 4, [2, 3, -1, -1]] and int(c.failed.item()) == 0
+
+
+# ---- more blocks than a wave has lanes -------------------------------------------------------------------
+# A wave looks up the pages of 64 blocks at a time, a lane each.
+
+
+def test_a_whole_prompt_past_a_waves_blocks():
+    """Tile attention with no split: workgroups that pass over up to 136 blocks look pages up three times, and the last
+    time for part of a wave."""
+    announce("kv attend, prompt of 4330")
+    n, heads = 4330, 8
+    r = Rig([n], heads, heads, 64, 32, "bf16", "e4m3", seed=55)
+    r.append([n])
+    # 34 tiles of rows on 8 heads: with n = 1 that is 272 items, past the 256 from which tokens are not split
+    q = torch.from_numpy(1.5 * r.rng.standard_normal((n, heads, 64))).bfloat16()
+    out = torch.full((n, heads, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(n, heads, device="cuda")
+    r.cache.attend(0, q.cuda(), out, _ids([0]), _ids([0, n]), n, lse=lse)
+    torch.cuda.synchronize()
+    for a, b in ((0, 40), (2040, 2060), (2170, 2180), (4090, 4110), (4290, 4330)):   # the oracle's loops are slow: some rows
+        ref, ref_lse, mass, reach = oracle.kv_attend(_f64(q[a:b]), r.k[0].values[:b], r.v[0].values[:b])
+        dx = reach * (68 * 2.0 ** -24 + 2.0 ** -23)
+        rel = np.expm1(2 * dx) + (n + 16) * 2.0 ** -24 + 2.0 ** -11
+        tol = rel[..., None] * mass + EPS["bf16"] * np.abs(ref) + 2.0 ** -30 * n * np.abs(r.v[0].values).max()
+        assert np.all(np.abs(_f64(out[a:b]) - ref) <= tol), f"rows {a} to {b}"
+        assert np.all(np.abs(_f64(lse[a:b]) - ref_lse) <= dx + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(ref_lse)))
+
+
+@pytest.mark.parametrize("heads, new, n, length", [((33, 1, 128), 1, 64, 35000), ((1, 1, 64), 1, 96, 80000)])
+def test_steps_past_a_waves_blocks(heads, new, n, length):
+    """Step attention in pieces of more than 256 blocks, four waves each: every wave looks pages up more than once, and the
+    last time for part of a wave.  The sequences share the pages of the first (forks), so the cache stays small; three of
+    them are compared."""
+    announce(f"kv attend, pieces past a wave's blocks {heads} {n} x {length}")
+    import activation_sparse_decode_relu_amd as pi
+    page = 128
+    lens = [length - 7 * i for i in range(n)]
+    r = Rig([length], *heads, page, "f16", "e4m3", seed=56)
+    r.append([length])
+    own = {name: getattr(r.cache, name) for name in ("k", "v", "k_exp", "v_exp")}
+    wide = pi.KVCache(*heads, r.cache.desc.pages, page, n, r.cache.table.shape[1], buffers=own)
+    wide.table.copy_(r.cache.table.expand(n, -1))
+    wide.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    q = torch.from_numpy(1.5 * r.rng.standard_normal((n * new, heads[0], heads[2]))).half()
+    out = torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
+    lse = torch.empty(n * new, heads[0], device="cuda")
+    wide.attend(0, q.cuda(), out, _ids(range(n)), _ids(range(0, n * new + 1, new)), new, lse=lse)
+    torch.cuda.synchronize()
+    k, v = list(r.k), list(r.v)
+    for i in (0, n // 2, n - 1):
+        for models, full in ((r.k, k), (r.v, v)):
+            m = oracle.KvModel(heads[1], heads[2], "e4m3", "f16")
+            m.values = full[0].values[:lens[i]]
+            models[0] = m
+        a, b = i * new, (i + 1) * new
+        r.compare(q[a:b], out[a:b], lse[a:b], [0, b - a], [0], 0, 0, None)
