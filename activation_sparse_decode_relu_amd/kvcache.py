@@ -170,8 +170,8 @@ class KVCache:
             stream.wait_stream(torch.cuda.current_stream(device.index))
         handle = _vp()
         buf = KvBuffers(*[getattr(self, name).data_ptr() for name, _ in KvBuffers._fields_])
-        check(LIB.pi_kv_create(_byref(d), _byref(buf), workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), self._stream(stream, ()), _byref(handle)))
+        self._run(LIB.pi_kv_create, _byref(d), _byref(buf), workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size(), self._stream(stream, ()), _byref(handle))
         self.handle = handle
 
     def close(self) -> None:
@@ -254,6 +254,14 @@ class KVCache:
                 getattr(self, name).record_stream(stream)
         return handle or None
 
+    def _run(self, fn, *args) -> None:
+        """Call the library on the cache's device: kernels start on the current one."""
+        if torch.cuda.current_device() == self.device.index:
+            check(fn(*args))
+        else:
+            with torch.cuda.device(self.device.index):
+                check(fn(*args))
+
     def _live(self):
         if self.handle is None:
             raise _invalid("the cache is closed")
@@ -273,8 +281,8 @@ class KVCache:
         rows = k.shape[0]
         vr = self._rows(v, "v", heads, rows)
         batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
-        check(LIB.pi_kv_append(self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
-                               self._stream(stream, (k, v, seqs, starts))))
+        self._run(LIB.pi_kv_append, self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
+                  self._stream(stream, (k, v, seqs, starts)))
 
     def read(self, layer, k_out, v_out, seqs, starts, first=None, stream=None) -> None:
         """Read tokens back: rows [starts[i], starts[i + 1]) of k_out and v_out get the tokens of seqs[i]
@@ -290,9 +298,9 @@ class KVCache:
         if first is not None:
             self._ids(first, "first", n)
         batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
-        check(LIB.pi_kv_read(self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
-                             None if first is None else first.data_ptr(),
-                             self._stream(stream, (k_out, v_out, seqs, starts, first))))
+        self._run(LIB.pi_kv_read, self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
+                  None if first is None else first.data_ptr(),
+                  self._stream(stream, (k_out, v_out, seqs, starts, first)))
 
     def attend(self, layer, q, out, seqs, starts, max_new, window=0, sinks=0, scale=None, lse=None, stream=None) -> None:
         """Attention of the last tokens of each sequence over the cache, which holds them already: row
@@ -315,8 +323,8 @@ class KVCache:
                             _in32(window, "window"), _in32(sinks, "sinks"),
                             d.head_dim ** -0.5 if scale is None else scale)
         batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
-        check(LIB.pi_kv_attend(self._live(), layer, _byref(args), _byref(batch),
-                               self._stream(stream, (q, out, seqs, starts, lse))))
+        self._run(LIB.pi_kv_attend, self._live(), layer, _byref(args), _byref(batch),
+                  self._stream(stream, (q, out, seqs, starts, lse)))
 
     # ---- pages ------------------------------------------------------------------------------------
 
@@ -327,23 +335,23 @@ class KVCache:
         not fit stays as it is, takes no tokens from append, and is counted in `failed` (check_failed)."""
         n = self._ids(seqs, "seqs")
         self._ids(counts, "counts", n)
-        check(LIB.pi_kv_reserve(self._live(), seqs.data_ptr(), counts.data_ptr(), n, self._stream(stream, (seqs, counts))))
+        self._run(LIB.pi_kv_reserve, self._live(), seqs.data_ptr(), counts.data_ptr(), n, self._stream(stream, (seqs, counts)))
 
     def free(self, seqs, stream=None) -> None:
         """Drop the sequences' pages: their table rows become -1, their lengths 0."""
         n = self._ids(seqs, "seqs")
-        check(LIB.pi_kv_free(self._live(), seqs.data_ptr(), n, self._stream(stream, (seqs,))))
+        self._run(LIB.pi_kv_free, self._live(), seqs.data_ptr(), n, self._stream(stream, (seqs,)))
 
     def fork(self, src, dst, stream=None) -> None:
         """Let dst[i] (which holds nothing) continue src[i] on the same pages, shared until one of them
         grows."""
         n = self._ids(src, "src")
         self._ids(dst, "dst", n)
-        check(LIB.pi_kv_fork(self._live(), src.data_ptr(), dst.data_ptr(), n, self._stream(stream, (src, dst))))
+        self._run(LIB.pi_kv_fork, self._live(), src.data_ptr(), dst.data_ptr(), n, self._stream(stream, (src, dst)))
 
     def compact(self, stream=None) -> None:
         """Move the pages in use to the front of the pool, in every layer; table and refs follow."""
-        check(LIB.pi_kv_compact(self._live(), self._stream(stream, ())))
+        self._run(LIB.pi_kv_compact, self._live(), self._stream(stream, ()))
 
     def check_failed(self) -> None:
         """Wait for the current stream and raise PiError if any reserve since the last check could not grow a sequence."""

@@ -1,5 +1,7 @@
 """The attention cache's binding without a GPU: arguments at the edges of their types, and whose memory a stream holds."""
 
+import contextlib
+import ctypes
 from types import SimpleNamespace
 
 import pytest
@@ -8,6 +10,7 @@ from test_kv_cpu import GOOD, _args, _cache, _rejects
 
 torch = pytest.importorskip("torch")
 pi = pytest.importorskip("activation_sparse_decode_relu_amd")
+from activation_sparse_decode_relu_amd import kvcache as kvc  # noqa: E402
 
 
 @pytest.mark.parametrize("value", [1 << 31, 1 << 32, (1 << 32) + 1, -(1 << 31) - 1, -(1 << 32)])
@@ -55,3 +58,53 @@ def test_a_stream_holds_the_caches_own_memory():
     assert arg.streams == [side, side]                  # another call's tensor, as far as the cache knows
     for name, m in mine.items():
         assert m.streams[:2] == [side, other], name
+
+
+# ---- devices -----------------------------------------------------------------------------------------------
+
+
+class _Second:
+    """The second of two devices; tensors of any count as its own."""
+    index = 1
+
+    def __eq__(self, other):
+        return True
+
+    def __ne__(self, other):
+        return False
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_run_on_the_caches_device(monkeypatch, current):
+    """Whatever device is the current one, the library is called with the cache's, and the current one is left as it was."""
+    now, calls = [current], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, now[0] = now[0], index
+        yield
+        now[0] = before
+
+    def recorder(name):
+        def fn(*args):
+            calls.append((name, now[0]))
+            return 0
+        return fn
+
+    names = ("append", "read", "attend", "reserve", "free", "fork", "compact")
+    monkeypatch.setattr(kvc, "LIB", SimpleNamespace(**{f"pi_kv_{n}": recorder(n) for n in names}))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: SimpleNamespace(cuda_stream=0))
+    c, a = _cache(), _args()
+    c.device, c.handle, c._met = _Second(), ctypes.c_void_p(), set()
+    for name in OWNED:
+        setattr(c, name, _Memory())
+    c.append(0, a.k, a.v, a.seqs, a.starts)
+    c.read(0, a.k, a.v, a.seqs, a.starts)
+    c.attend(0, a.q, a.out, a.seqs, a.starts, 1)
+    c.reserve(a.seqs, a.seqs)
+    c.free(a.seqs)
+    c.fork(a.seqs, a.seqs)
+    c.compact()
+    assert calls == [(n, 1) for n in names] and now == [current]
