@@ -79,11 +79,11 @@ _declare()
 _byref = ctypes.byref
 
 
-def _in32(value, name):
-    """A number that the C ABI takes in 32 bits: ctypes would cut one that does not fit."""
-    if not -0x80000000 <= value <= 0x7fffffff:
-        raise _invalid(f"{name}={value} does not fit in 32 bits")
-    return value
+def _in32(**numbers) -> None:
+    """Refuse numbers that the C ABI takes in 32 bits and that do not fit: ctypes would cut them."""
+    for name, value in numbers.items():
+        if not -0x80000000 <= value <= 0x7fffffff:
+            raise _invalid(f"{name}={value} does not fit in 32 bits")
 
 
 def kv_desc(heads, kv_heads, head_dim, pages, page_tokens, max_seqs, max_seq_pages, layers=1, act_dtype="f16",
@@ -92,7 +92,9 @@ def kv_desc(heads, kv_heads, head_dim, pages, page_tokens, max_seqs, max_seq_pag
     c = CODES[code] if isinstance(code, str) else int(code)
     sizes = dict(heads=heads, kv_heads=kv_heads, head_dim=head_dim, page_tokens=page_tokens, pages=pages, layers=layers,
                  max_seqs=max_seqs, max_seq_pages=max_seq_pages, act_dtype=act, code=c)
-    return KvDesc(*[_in32(int(value), name) for name, value in sizes.items()])
+    sizes = {name: int(value) for name, value in sizes.items()}
+    _in32(**sizes)
+    return KvDesc(*sizes.values())
 
 
 def kv_workspace_bytes(desc: KvDesc) -> int:
@@ -162,7 +164,7 @@ class KVCache:
         if not isinstance(workspace, torch.Tensor) or workspace.device != device or not workspace.is_contiguous():
             raise _invalid(f"workspace must be a contiguous tensor on {device}")
         self.workspace = workspace
-        self._met = set()
+        self._met, self._lone = set(), torch.cuda.device_count() == 1
         if device.type != "cuda":
             raise _invalid(f"the cache must be on a CUDA device, not {device}")
         self._act = _ACT_TORCH[d.act_dtype]
@@ -256,7 +258,7 @@ class KVCache:
 
     def _run(self, fn, *args) -> None:
         """Call the library on the cache's device: kernels start on the current one."""
-        if torch.cuda.current_device() == self.device.index:
+        if self._lone or torch.cuda.current_device() == self.device.index:
             check(fn(*args))
         else:
             with torch.cuda.device(self.device.index):
@@ -274,30 +276,32 @@ class KVCache:
         [rows][kv_heads][head_dim] are the last of the lens[seqs[i]] tokens of seqs[i] (reserve has
         counted them).  A sequence that reserve refused stores nothing.  Blocks of 32 tokens and a head
         share an exponent: see pi_kv.h."""
-        layer = _in32(layer, "layer")
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k, "k", heads)
         rows = k.shape[0]
         vr = self._rows(v, "v", heads, rows)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
+        if (layer | rows) >> 31:   # below 0, or too large for some
+            _in32(layer=layer, rows=rows)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
         self._run(LIB.pi_kv_append, self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
                   self._stream(stream, (k, v, seqs, starts)))
 
     def read(self, layer, k_out, v_out, seqs, starts, first=None, stream=None) -> None:
         """Read tokens back: rows [starts[i], starts[i + 1]) of k_out and v_out get the tokens of seqs[i]
         from first[i] on (from 0 where first is None); tokens past the end or before the first read as 0."""
-        layer = _in32(layer, "layer")
         n, heads = self._ids(seqs, "seqs"), self.desc.kv_heads
         self._ids(starts, "starts", n + 1)
         kr = self._rows(k_out, "k_out", heads)
         rows = k_out.shape[0]
         vr = self._rows(v_out, "v_out", heads, rows)
+        if (layer | rows) >> 31:
+            _in32(layer=layer, rows=rows)
         self._writable(k_out, "k_out")
         self._writable(v_out, "v_out")
         if first is not None:
             self._ids(first, "first", n)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
         self._run(LIB.pi_kv_read, self._live(), layer, _byref(kr), _byref(vr), _byref(batch),
                   None if first is None else first.data_ptr(),
                   self._stream(stream, (k_out, v_out, seqs, starts, first)))
@@ -310,7 +314,6 @@ class KVCache:
         denominator.  max_new: at least the largest count of rows of a sequence (rows past it are not
         computed).  scale: head_dim ** -0.5 unless given."""
         d = self.desc
-        layer = _in32(layer, "layer")
         n = self._ids(seqs, "seqs")
         self._ids(starts, "starts", n + 1)
         qr = self._rows(q, "q", d.heads)
@@ -319,10 +322,11 @@ class KVCache:
         self._writable(out, "out")
         if lse is not None:
             self._dense(lse, "lse", torch.float32, (rows, d.heads))
-        args = KvAttendArgs(qr, orow, None if lse is None else lse.data_ptr(), _in32(max_new, "max_new"),
-                            _in32(window, "window"), _in32(sinks, "sinks"),
+        if (layer | rows | max_new | window | sinks) >> 31:
+            _in32(layer=layer, rows=rows, max_new=max_new, window=window, sinks=sinks)
+        args = KvAttendArgs(qr, orow, None if lse is None else lse.data_ptr(), max_new, window, sinks,
                             d.head_dim ** -0.5 if scale is None else scale)
-        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, _in32(rows, "rows"))
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
         self._run(LIB.pi_kv_attend, self._live(), layer, _byref(args), _byref(batch),
                   self._stream(stream, (q, out, seqs, starts, lse)))
 

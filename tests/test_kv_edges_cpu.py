@@ -97,7 +97,7 @@ def test_calls_run_on_the_caches_device(monkeypatch, current):
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: SimpleNamespace(cuda_stream=0))
     c, a = _cache(), _args()
-    c.device, c.handle, c._met = _Second(), ctypes.c_void_p(), set()
+    c.device, c.handle, c._met, c._lone = _Second(), ctypes.c_void_p(), set(), False
     for name in OWNED:
         setattr(c, name, _Memory())
     c.append(0, a.k, a.v, a.seqs, a.starts)
