@@ -50,9 +50,10 @@ __global__ __launch_bounds__(256) void k_kv_fork(const KvPool P, const int* __re
 
 // What one sequence of a reserve call needs.
 struct Need {
-  int s, len, end, have, pages;   // pages: new ones, a copy's among them; -1: cannot grow
-  int shared;                     // the last page, if it has to be copied, else -1
-  bool named;                     // columns past the length name pages: a caller has lowered it
+  int s = 0, count = 0, len = 0, end = 0, have = 0;
+  int pages = 0;        // new ones, a copy's among them; -1: cannot grow
+  int shared = -1;      // the last page, if it has to be copied, else -1
+  bool named = false;   // columns past the length name pages: a caller has lowered it
 };
 
 // The page that a column past a sequence's length still names and that no other entry does: it is used again.
@@ -64,10 +65,7 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   Need r;
   r.s = seqs[i];
   r.pages = -1;
-  r.shared = -1;
-  r.named = false;
-  r.len = r.end = r.have = 0;
-  const int c = counts[i];
+  const int c = r.count = counts[i];
   if (r.s < 0 || r.s >= P.max_seqs) return r;
   r.len = P.lens[r.s];
   if (r.len < 0 || c < 0) return r;
@@ -76,27 +74,23 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   r.end = (int)end;
   r.have = (r.len + P.page_tokens - 1) / P.page_tokens;
   const int cols = (r.end + P.page_tokens - 1) / P.page_tokens - r.have;
-  if (c > 0 && r.len % P.page_tokens != 0) {
-    const int last = P.table[(size_t)r.s * P.max_pages + r.have - 1];
-    if (last < 0 || last >= P.pages) return r;
-    if (P.refs[last] > 1) r.shared = last;
-  }
+  const int* row = P.table + (size_t)r.s * P.max_pages + r.have;
+  const bool part = c > 0 && r.len % P.page_tokens != 0;
+  const int last = part ? row[-1] : 0, next = cols > 0 ? row[0] : -1;   // on their way together
+  if (last < 0 || last >= P.pages) return r;
+  if (part && P.refs[last] > 1) r.shared = last;
   // columns never name more pages than there are; one too many is as good as any number that cannot be had, and
   // keeps the call's sum in 32 bits
   r.pages = min(cols, P.pages + 1);
   if (r.pages <= P.pages) {
-    const int* row = P.table + (size_t)r.s * P.max_pages + r.have;
-    for (int j = 0; j < cols; j += 8) {
-      int p[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = j + e < cols ? row[j + e] : -1;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (p[e] >= 0) {
-          r.named = true;
-          r.pages -= keeps(P, p[e]) ? 1 : 0;
-        }
-    }
+    auto count = [&](int page) {
+      if (page < 0) return;
+      r.named = true;
+      r.pages -= keeps(P, page) ? 1 : 0;
+    };
+    count(next);
+#pragma unroll 4
+    for (int j = 1; j < cols; ++j) count(row[j]);
   }
   r.pages += r.shared >= 0 ? 1 : 0;
   return r;
@@ -134,10 +128,10 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   if (tid == 0) s_failed = s_given = 0;
   // how many pages the call wants in all
   int want = 0;
-  Need mine{0, 0, 0, 0, 0, -1, false};   // of the first kPlan sequences: seldom are there more
+  Need mine;   // of the first kPlan sequences: seldom are there more
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    const Need r = i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1, false};
+    const Need r = i < n ? need_of(P, seqs, counts, i) : Need{};
     if (base == 0) mine = r;
     int total;
     block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
@@ -151,7 +145,7 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   int given = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{0, 0, 0, 0, 0, -1, false};
+    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{};
     int total;
     const int at = given + block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
     const bool grows = i < n && r.pages >= 0 && at + r.pages <= found;
@@ -179,15 +173,16 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
       P.src[i] = from;
       P.dst[i] = to;
       // see k_kv_append; a request for no tokens says nothing about those of another
-      if (r.s >= 0 && r.s < P.max_seqs && counts[i] > 0) P.refused[r.s] = grows ? 0 : r.len + 1;
+      if (r.s >= 0 && r.s < P.max_seqs && r.count > 0) P.refused[r.s] = grows ? 0 : r.len + 1;
     }
     given = min(given + total, P.pages + 1);
   }
   __threadfence_block();
   __syncthreads();
   for (int k = tid; k < s_given; k += kPlan) {   // all up to the last: who comes after one that fails fails too
-    P.refs[P.list[k]] = 1;
-    if (P.drop[k] >= 0) atomicSub(P.refs + P.drop[k], 1);
+    const int taken = P.list[k], left = P.drop[k];
+    P.refs[taken] = 1;
+    if (left >= 0) atomicSub(P.refs + left, 1);
   }
   if (tid == 0) {
     *P.count = n;
