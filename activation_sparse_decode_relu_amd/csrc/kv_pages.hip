@@ -50,17 +50,18 @@ __global__ __launch_bounds__(256) void k_kv_fork(const KvPool P, const int* __re
 
 // What one sequence of a reserve call needs.
 struct Need {
-  int s = 0, count = 0, len = 0, end = 0, have = 0;
+  int s = 0, count = 0, len = 0, end = 0, have = 0, cols = 0;   // cols: the columns from `have` on that it grows into
   int pages = 0;        // new ones, a copy's among them; -1: cannot grow
   int shared = -1;      // the last page, if it has to be copied, else -1
-  bool named = false;   // columns past the length name pages: a caller has lowered it
 };
 
-// The page that a column past a sequence's length still names and that no other entry does: it is used again.
+// A column past a sequence's length may still name a page (a caller has lowered the length): one that no other entry
+// names is used again.
 __device__ __forceinline__ bool keeps(const KvPool& P, int page) {
   return page >= 0 && page < P.pages && P.refs[page] == 1;
 }
 
+// All but what such columns save.
 __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const int* counts, int i) {
   Need r;
   r.s = seqs[i];
@@ -73,26 +74,48 @@ __device__ __forceinline__ Need need_of(const KvPool& P, const int* seqs, const 
   if (end > (long long)P.max_pages * P.page_tokens) return r;
   r.end = (int)end;
   r.have = (r.len + P.page_tokens - 1) / P.page_tokens;
-  const int cols = (r.end + P.page_tokens - 1) / P.page_tokens - r.have;
-  const int* row = P.table + (size_t)r.s * P.max_pages + r.have;
-  const bool part = c > 0 && r.len % P.page_tokens != 0;
-  const int last = part ? row[-1] : 0, next = cols > 0 ? row[0] : -1;   // on their way together
-  if (last < 0 || last >= P.pages) return r;
-  if (part && P.refs[last] > 1) r.shared = last;
-  // columns never name more pages than there are; one too many is as good as any number that cannot be had, and
-  // keeps the call's sum in 32 bits
-  r.pages = min(cols, P.pages + 1);
-  if (r.pages <= P.pages) {
-    auto count = [&](int page) {
-      if (page < 0) return;
-      r.named = true;
-      r.pages -= keeps(P, page) ? 1 : 0;
-    };
-    count(next);
-#pragma unroll 4
-    for (int j = 1; j < cols; ++j) count(row[j]);
+  r.cols = (r.end + P.page_tokens - 1) / P.page_tokens - r.have;
+  if (c > 0 && r.len % P.page_tokens != 0) {
+    const int last = P.table[(size_t)r.s * P.max_pages + r.have - 1];
+    if (last < 0 || last >= P.pages) return r;
+    if (P.refs[last] > 1) r.shared = last;
   }
-  r.pages += r.shared >= 0 ? 1 : 0;
+  // the columns of a row name no more pages than there are; one too many is as good as any number that cannot be had,
+  // and keeps the call's sum in 32 bits
+  r.pages = min(r.cols, P.pages + 1) + (r.shared >= 0 ? 1 : 0);
+  return r;
+}
+
+// The needs of sequences base .. base + kPlan, one a thread, by the whole workgroup.  The columns are looked through by
+// a wave for each sequence (a thread for each took 26 us for the 128 of one prompt); sets `named` where any names a page.
+__device__ Need needs_of(const KvPool& P, const int* seqs, const int* counts, int n, int base, int* named) {
+  __shared__ int s_cols[kPlan], s_kept[kPlan];
+  __shared__ long long s_row[kPlan];
+  const int tid = threadIdx.x, lane = tid & (WAVE - 1), i = base + tid;
+  Need r = i < n ? need_of(P, seqs, counts, i) : Need{};
+  const bool look = r.cols > 0 && r.pages >= 0 && r.pages <= P.pages;
+  if (!__syncthreads_or(look)) return r;
+  s_cols[tid] = look ? r.cols : 0;
+  s_row[tid] = (long long)r.s * P.max_pages + r.have;
+  s_kept[tid] = 0;
+  __syncthreads();
+  const int most = min(n - base, kPlan);
+  for (int q = tid / WAVE; q < most; q += kPlan / WAVE) {
+    const int cols = s_cols[q];
+    const int* row = P.table + s_row[q];
+    int kept = 0;
+#pragma unroll 4
+    for (int j = lane; j < cols; j += WAVE) {
+      const int page = row[j];
+      if (page >= 0) {
+        *named = 1;
+        kept += keeps(P, page) ? 1 : 0;
+      }
+    }
+    if (kept > 0) atomicAdd(&s_kept[q], kept);
+  }
+  __syncthreads();
+  r.pages -= s_kept[tid];
   return r;
 }
 
@@ -123,15 +146,15 @@ __device__ int list_free(const KvPool& P, int want) {
 
 __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int* __restrict__ seqs,
                                                       const int* __restrict__ counts, int n) {
-  __shared__ int s_failed, s_given;
+  __shared__ int s_failed, s_given, s_named;
   const int tid = threadIdx.x;
-  if (tid == 0) s_failed = s_given = 0;
+  if (tid == 0) s_failed = s_given = s_named = 0;
+  __syncthreads();
   // how many pages the call wants in all
   int want = 0;
-  Need mine;   // of the first kPlan sequences: seldom are there more
+  Need mine;                             // of the first kPlan sequences: seldom are there more
   for (int base = 0; base < n; base += kPlan) {
-    const int i = base + tid;
-    const Need r = i < n ? need_of(P, seqs, counts, i) : Need{};
+    const Need r = needs_of(P, seqs, counts, n, base, &s_named);
     if (base == 0) mine = r;
     int total;
     block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
@@ -140,12 +163,13 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   const int found = list_free(P, want);
   __threadfence_block();
   __syncthreads();
-  // hand them out in order; what a sequence needs is worked out before anything of it changes, and
-  // every page keeps its count until all have been looked at
+  // Hand them out in order; what a sequence needs is worked out before anything of it changes, and shared pages keep
+  // their counts until all have been looked at.  Where columns name pages already, all pages do.
+  const bool named = s_named != 0;
   int given = 0;
   for (int base = 0; base < n; base += kPlan) {
     const int i = base + tid;
-    const Need r = base == 0 ? mine : i < n ? need_of(P, seqs, counts, i) : Need{};
+    const Need r = base == 0 ? mine : needs_of(P, seqs, counts, n, base, &s_named);
     int total;
     const int at = given + block_exclusive_scan<kPlan>(max(r.pages, 0), &total);
     const bool grows = i < n && r.pages >= 0 && at + r.pages <= found;
@@ -156,17 +180,29 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
       int k = at, j = r.have;
       if (r.shared >= 0) {
         from = r.shared;
-        to = P.list[k++];
+        to = P.list[k];
         row[r.have - 1] = to;
-        P.drop[at] = from;
+        if (named)
+          P.drop[k] = -1;
+        else
+          P.refs[to] = 1;
+        ++k;
       }
-      for (; k < at + r.pages && j < P.max_pages; ++j) {
-        const int old = r.named ? row[j] : -1;
-        if (keeps(P, old)) continue;
-        P.drop[k] = old >= 0 && old < P.pages && P.refs[old] > 1 ? old : -1;
-        row[j] = P.list[k++];
+      if (named) {
+        for (; k < at + r.pages && j < r.have + r.cols; ++j) {
+          const int old = row[j];
+          if (keeps(P, old)) continue;
+          P.drop[k] = old >= 0 && old < P.pages && P.refs[old] > 1 ? old : -1;
+          row[j] = P.list[k++];
+        }
+        atomicMax(&s_given, at + r.pages);
+      } else {
+        for (; k < at + r.pages; ++k, ++j) {
+          const int p = P.list[k];
+          row[j] = p;
+          P.refs[p] = 1;
+        }
       }
-      atomicMax(&s_given, at + r.pages);
       P.lens[r.s] = r.end;
     }
     if (i < n) {
@@ -179,7 +215,10 @@ __global__ __launch_bounds__(kPlan) void k_kv_reserve(const KvPool P, const int*
   }
   __threadfence_block();
   __syncthreads();
-  for (int k = tid; k < s_given; k += kPlan) {   // all up to the last: who comes after one that fails fails too
+  for (int i = tid; i < n; i += kPlan)
+    if (P.src[i] >= 0) atomicSub(P.refs + P.src[i], 1);
+  // those handed out are the first of the list: who comes after one that fails fails too
+  for (int k = tid; named && k < s_given; k += kPlan) {
     const int taken = P.list[k], left = P.drop[k];
     P.refs[taken] = 1;
     if (left >= 0) atomicSub(P.refs + left, 1);

@@ -277,3 +277,33 @@ def test_tokens_after_a_rollback():
         err = (t.double() - sign * want.double()).abs()
         assert bool((err <= 2.0 ** -4 * want.double().abs() + 2.0 ** -16).all())
     assert int((c.refs > 0).sum()) == 3
+
+
+def test_rollbacks_of_more_sequences_than_threads():
+    """1500 sequences, some of them forks, every third set back; then one that grows by more columns than a wave has lanes."""
+    announce("kv reserve, 1500 sequences with rollbacks")
+    rng = np.random.default_rng(32)
+    n, pages, width = 1500, 7000, 100
+    c = _cache(pages, seqs=n, width=width)
+    model = _state(c)
+    table, lens, refs = model
+    order = rng.permutation(n).tolist()
+    _reserve(c, model, order[:1200], [int(x) for x in rng.integers(1, 150, 1200)], 32)
+    oracle.kv_fork(*model, order[:300], order[1200:])
+    c.fork(_ids(order[:300]), _ids(order[1200:]))
+    for s in range(0, n, 3):
+        lens[s] = int(rng.integers(0, lens[s] + 1))
+    c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    _reserve(c, model, rng.permutation(n).tolist(), [int(x) for x in rng.integers(0, 70, n)], 32)
+    assert _counts_hold(model)
+    long = order[-1]
+    for value in (32 * width, 40):
+        _reserve(c, model, [long, order[0]], [value - lens[long], 1], 32)
+        assert lens[long] == value and _counts_hold(model)
+        lens[long] = 7
+        c.lens[long] = 7
+    _reserve(c, model, [long], [32 * width - 7], 32)
+    assert lens[long] == 32 * width and _counts_hold(model)
+    oracle.kv_free(*model, list(range(n)))
+    c.free(_ids(range(n)))
+    assert _state(c) == model and not any(refs)
