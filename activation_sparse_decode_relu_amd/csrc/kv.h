@@ -107,7 +107,7 @@ struct KvPool {
   int* src;            // workspace: pages to copy from and to, -1 for none [max(pages, max_seqs)]
   int* dst;
   int* list;           // workspace: reserve's free pages, compact's new places [pages]
-  int* drop;           // workspace: the shared page that each of reserve's pages takes the place of, or -1 [pages]
+  int* drop;           // workspace: the shared page, past a lowered length, whose column each of list gets, or -1 [pages]
   int* count;          // workspace: how many copies
   int64_t page_bytes;  // of k and of v
   int exp_bytes;       // a page's exponents, of k and of v
