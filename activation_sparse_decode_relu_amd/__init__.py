@@ -1,7 +1,8 @@
-"""Activation-sparse ReLU FFN decode, and attention over an 8-bit paged cache, on MI355X (gfx950).
+"""Activation-sparse ReLU FFN decode, attention over an 8-bit paged cache, and products with 4-bit weights, on MI355X
+(gfx950).
 
 The compute lives in libpi_ffn.so (hand-written HIP kernels behind the C ABIs in
-include/pi_ffn.h and include/pi_kv.h); this package is its thin Python binding.
+include/pi_ffn.h, include/pi_kv.h and include/pi_linear.h); this package is its thin Python binding.
 """
 
 from .binding import (  # noqa: F401
@@ -23,3 +24,4 @@ from .binding import (  # noqa: F401
     workspace_bytes,
 )
 from .kvcache import KV_EXPORTED, KVCache, kv_desc, kv_workspace_bytes  # noqa: F401
+from .linear import LINEAR_EXPORTED, Linear, linear_desc, linear_packed_bytes  # noqa: F401

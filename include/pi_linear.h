@@ -1,0 +1,83 @@
+/*
+ * pi_linear.h -- C ABI of products with 4-bit weights (gfx950), in libpi_ffn.so.
+ *
+ * The projections of an attention layer, for a step of one token or many and for prompts:
+ *
+ *   y[t] = W x[t] + bias + add[t]          W [d_out][d_in] in q4g32, the FFN's format (pi_ffn.h)
+ *
+ * Weights are laid out once, by pi_linear_create, in the order in which the matrix instructions take them;
+ * the q4g32 rows are not needed afterwards.
+ *
+ * Layout of the packed weights
+ * ----------------------------
+ * [ceil(d_out / 16)][ceil(d_in / 256)] slabs of 2304 bytes: two KB of codes, one for each 128 columns, and fp16
+ * scales [16 rows][8 groups].  Word j of the 16 bytes 16 l .. of a KB holds the columns 32 j + 8 (l / 16) .. + 8
+ * of row l % 16, as u = q + 8: column 2 i at bit 4 i and column 2 i + 1 at bit 16 + 4 i, the word rotated left
+ * by 6 bits (fp16 activations) or 3 (bf16).  Rows and columns that are not there have q = 0 and scale 0.
+ *
+ * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
+ * --------------------------------------------------------------------------------------------------
+ * - Ownership: the caller allocates all device memory; a handle borrows it until pi_linear_destroy.
+ * - Streams: calls only enqueue on `stream`.  A handle has no workspace: its calls may run at the same time.
+ * - Products of whole numbers and activations are summed in fp32 by groups of 32, and the groups' sums, times
+ *   their scales, in fp32; y is rounded once.  A row's result depends on its own x, and, in its last bits, on
+ *   the number of rows of the call; it does not depend on the order in which workgroups run.
+ * - A row of x that holds an infinity, a NaN, or (bf16) a magnitude of 2^118 and more may come out as NaN, other
+ *   rows are not touched by it.
+ */
+#ifndef PI_LINEAR_H
+#define PI_LINEAR_H
+
+#include "pi_ffn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define PI_LINEAR_ABI_VERSION 1
+
+typedef enum pi_linear_act { PI_LINEAR_F16 = 0, PI_LINEAR_BF16 = 1 } pi_linear_act;
+
+typedef struct pi_linear_desc {
+  int32_t d_in;      /* a multiple of 32, up to 2^20 */
+  int32_t d_out;     /* 1 to 2^24                    */
+  int32_t act_dtype; /* pi_linear_act: type of x, add and y */
+} pi_linear_desc;
+
+/* Rows of a call: y may be add itself, and else overlaps neither x nor add. */
+typedef struct pi_linear_args {
+  const void* x;      /* [rows][d_in], 16-byte aligned                                      */
+  const void* add;    /* [rows][d_out] or NULL                                              */
+  void* y;            /* [rows][d_out]                                                      */
+  int64_t x_stride;   /* from row to row, in elements: a multiple of 8 (looked at for several rows) */
+  int64_t add_stride; /* in elements                                                        */
+  int64_t y_stride;   /* in elements, at least d_out                                        */
+  int32_t rows;       /* 0 to 2^24; 0 enqueues nothing                                      */
+} pi_linear_args;
+
+typedef struct pi_linear pi_linear;
+
+/* ABI version of this part of the library (PI_LINEAR_ABI_VERSION). */
+int32_t pi_linear_abi_version(void);
+
+/* Bytes of device memory the packed weights take.  Host only. */
+pi_status pi_linear_packed_bytes(const pi_linear_desc* desc, size_t* bytes);
+
+/*
+ * Lay the weights w (q4g32 [d_out][d_in / 2], 4-byte aligned) and scales (fp16 [d_out][d_in / 32]) out in
+ * `packed` (256-byte aligned) on `stream`, and bind that and bias (fp32 [d_out] or NULL) to a new handle.
+ */
+pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void* scales, const float* bias, void* packed,
+                           size_t packed_bytes, void* stream, pi_linear** out);
+
+/* Release the handle (host memory only). */
+pi_status pi_linear_destroy(pi_linear* h);
+
+/* y = W x + bias + add for every row. */
+pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* PI_LINEAR_H */

@@ -1,0 +1,149 @@
+"""Products with 4-bit weights without a GPU: the C ABI's symbols and refusals, and the binding's checks."""
+
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pi = pytest.importorskip("activation_sparse_decode_relu_amd")
+from activation_sparse_decode_relu_amd import linear as lin  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "pi_linear.h")
+FAKE = 0x10000
+
+
+def _declared():
+    return sorted(set(re.findall(r"^\s*(?:pi_status|int32_t)\s+(pi_linear_\w+)\s*\(", open(HEADER).read(), re.M)))
+
+
+def test_symbols():
+    assert set(_declared()) == set(pi.LINEAR_EXPORTED)
+    for name in _declared():
+        assert hasattr(pi.LIB, name), f"{name} is declared in pi_linear.h but not exported"
+    assert pi.LIB.pi_linear_abi_version() == lin.LINEAR_ABI_VERSION
+
+
+def test_header_is_plain_c(tmp_path):
+    for cc, flags in (("gcc", ["-std=c99", "-xc"]), ("g++", ["-std=c++17", "-xc++"])):
+        src = tmp_path / "use.c"
+        src.write_text('#include "pi_linear.h"\nint main(void) { pi_linear_desc d; (void)d; return PI_LINEAR_ABI_VERSION - 1; }\n')
+        subprocess.run([cc, *flags, "-Wall", "-Wextra", "-Werror", "-pedantic", "-fsyntax-only", "-I",
+                        os.path.join(ROOT, "include"), str(src)], check=True)
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(lin.LinearDesc) == 12
+    assert ctypes.sizeof(lin.LinearArgs) == 56
+
+
+@pytest.mark.parametrize("d_in, d_out, tiles, slabs", [(32, 1, 1, 1), (256, 16, 1, 1), (288, 17, 2, 2), (8192, 10240, 640, 32)])
+def test_packed_bytes(d_in, d_out, tiles, slabs):
+    assert pi.linear_packed_bytes(pi.linear_desc(d_in, d_out)) == tiles * slabs * 2304
+
+
+@pytest.mark.parametrize("bad", [dict(d_in=0), dict(d_in=48), dict(d_in=-32), dict(d_in=(1 << 20) + 32), dict(d_out=0),
+                                 dict(d_out=(1 << 24) + 1), dict(act_dtype=2), dict(act_dtype=-1)])
+def test_bad_descriptors(bad):
+    with pytest.raises(pi.PiError) as e:
+        pi.linear_packed_bytes(pi.linear_desc(**{**dict(d_in=64, d_out=8), **bad}))
+    assert e.value.status == 1 and pi.last_error()
+
+
+def test_numbers_past_32_bits():
+    with pytest.raises(pi.PiError):
+        pi.linear_desc(1 << 32, 8)
+    with pytest.raises(KeyError):
+        pi.linear_desc(64, 8, "f32")
+
+
+@pytest.mark.parametrize("change, status", [
+    (dict(w=None), 1), (dict(w=FAKE + 2), 1), (dict(scales=None), 1), (dict(scales=FAKE + 1), 1), (dict(bias=FAKE + 2), 1),
+    (dict(packed=None), 2), (dict(packed=FAKE + 16), 2), (dict(size=2303), 2)])
+def test_create_refusals(change, status):
+    a = {**dict(w=FAKE, scales=FAKE, bias=None, packed=FAKE, size=2304), **change}
+    d, h = pi.linear_desc(64, 8), ctypes.c_void_p()
+    st = pi.LIB.pi_linear_create(ctypes.byref(d), a["w"], a["scales"], a["bias"], a["packed"], a["size"], None, ctypes.byref(h))
+    assert st == status and not h.value
+
+
+def test_null_handles():
+    a, h = lin.LinearArgs(), ctypes.c_void_p()
+    assert pi.LIB.pi_linear_forward(None, ctypes.byref(a), None) == 1
+    assert pi.LIB.pi_linear_destroy(None) == 1
+    assert pi.LIB.pi_linear_create(None, None, None, None, None, 0, None, ctypes.byref(h)) == 1
+    assert pi.LIB.pi_linear_packed_bytes(None, None) == 1
+
+
+class _Handle:
+    """A handle as the library lays it out, for refusals that come before anything is enqueued: desc, packed, bias."""
+
+    def __init__(self, d_in, d_out):
+        class Raw(ctypes.Structure):
+            _fields_ = [("desc", lin.LinearDesc), ("packed", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+        self.raw = Raw(pi.linear_desc(d_in, d_out), FAKE, None)
+
+    def forward(self, **change):
+        a = {**dict(x=FAKE, add=None, y=FAKE, x_stride=64, add_stride=0, y_stride=8, rows=2), **change}
+        return pi.LIB.pi_linear_forward(ctypes.byref(self.raw), ctypes.byref(lin.LinearArgs(**a)), None)
+
+
+@pytest.mark.parametrize("change", [dict(rows=-1), dict(rows=(1 << 24) + 1), dict(x=None), dict(x=FAKE + 8), dict(y=None),
+                                    dict(y=FAKE + 1), dict(add=FAKE + 1), dict(x_stride=68), dict(x_stride=-64),
+                                    dict(add=FAKE, add_stride=-8), dict(y_stride=7)])
+def test_forward_refusals(change):
+    assert _Handle(64, 8).forward(**change) == 1 and pi.last_error()
+
+
+def test_no_rows_enqueue_nothing():
+    assert _Handle(64, 8).forward(rows=0, x=None, y=None) == 0
+
+
+# ---- the binding -----------------------------------------------------------------------------------
+
+
+def _closed(act="f16"):
+    m = object.__new__(pi.Linear)
+    m.desc, m.handle, m.device = pi.linear_desc(64, 8, act), ctypes.c_void_p(), torch.device("cpu")
+    m._act = lin._ACT_TORCH[m.desc.act_dtype]
+    return m
+
+
+def _rejects(fn, needle):
+    with pytest.raises(pi.PiError) as e:
+        fn()
+    assert e.value.status == 1 and needle in str(e.value), str(e.value)
+
+
+@pytest.mark.parametrize("x, y, add, needle", [
+    (None, (5, 8), None, "x must be a torch tensor"), ((5, 32), (5, 8), None, "x must be [rows][64]"),
+    ((5, 64), (4, 8), None, "y must be [5][8]"), ((5, 64), (5, 8), (5, 64), "add must be [5][8]")])
+def test_shapes(x, y, add, needle):
+    make = lambda s: None if s is None else torch.zeros(s, dtype=torch.float16)  # noqa: E731
+    _rejects(lambda: _closed().forward(make(x), make(y), make(add)), needle)
+
+
+def test_tensor_refusals():
+    m, h = _closed(), torch.float16
+    x, y = torch.zeros(5, 64, dtype=h), torch.zeros(5, 8, dtype=h)
+    _rejects(lambda: m.forward(x.bfloat16(), y), "x is torch.bfloat16")
+    _rejects(lambda: m.forward(x, y.float()), "y is torch.float32")
+    _rejects(lambda: m.forward(torch.zeros(5, 128, dtype=h)[:, ::2], y), "innermost")
+    _rejects(lambda: m.forward(x, y[:1].expand(5, 8)), "overlap")
+    _rejects(lambda: m.forward(x.to("meta"), y), "x is on meta")
+    m.handle = None
+    _rejects(lambda: m.forward(x, y), "closed")
+
+
+def test_weights_are_checked():
+    w, s = torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.float16)
+    _rejects(lambda: pi.Linear(w, s), "CUDA")
+    _rejects(lambda: pi.Linear(w.float(), s), "w is torch.float32")
+    _rejects(lambda: pi.Linear(w, s.T), "scales must be")
+    _rejects(lambda: pi.Linear(w, s, bias=torch.zeros(9)), "bias must be [8]")
+    _rejects(lambda: pi.Linear(w, None), "scales must be a torch tensor")
+    _rejects(lambda: pi.Linear(w[0], s), "w must be")
+    _rejects(lambda: pi.Linear(w[:, :8], s), "d_in=16 must be")
