@@ -23,5 +23,5 @@ from .binding import (  # noqa: F401
     upload_layer,
     workspace_bytes,
 )
-from .kvcache import KV_EXPORTED, KVCache, kv_desc, kv_workspace_bytes  # noqa: F401
+from .kvcache import KV_EXPORTED, ROPE_EXPORTED, KVCache, Rope, kv_desc, kv_workspace_bytes  # noqa: F401
 from .linear import LINEAR_EXPORTED, Linear, linear_desc, linear_packed_bytes  # noqa: F401

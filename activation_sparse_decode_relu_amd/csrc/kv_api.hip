@@ -8,6 +8,7 @@
 
 #include "kernels.h"
 #include "kv.h"
+#include "kv_rotate.h"
 #include "pi_kv.h"
 #include "status.h"
 
@@ -75,7 +76,54 @@ struct pi_kv {
   size_t exp_bytes() const { return (size_t)desc.kv_heads * (desc.page_tokens / PI_KV_BLOCK); }
 };
 
+struct pi_rope {
+  pi_rope_desc desc;
+  double freqs[pik::kMaxPairs];
+  uint64_t turns[pik::kMaxPairs];   // f / 2 pi in 2^-64
+};
+
 namespace {
+
+constexpr double kPi = 3.14159265358979323846;
+
+pi_status check_rope(const pi_rope_desc* d) {
+  if (d == nullptr) return fail(PI_ERR_INVALID, "desc is NULL");
+  if (d->head_dim != 64 && d->head_dim != 128)
+    return fail(PI_ERR_UNSUPPORTED, "head_dim=%d: the kernels take 64 or 128", d->head_dim);
+  if (d->rot_dims < 0 || d->rot_dims > d->head_dim || d->rot_dims % 2 != 0)
+    return fail(PI_ERR_INVALID, "rot_dims=%d must be even and lie in [0, head_dim=%d]", d->rot_dims, d->head_dim);
+  if (d->rot_dims % 16 != 0) return fail(PI_ERR_UNSUPPORTED, "rot_dims=%d: the kernels take multiples of 16", d->rot_dims);
+  if (d->layout != PI_ROPE_HALF && d->layout != PI_ROPE_INTERLEAVED)
+    return fail(PI_ERR_INVALID, "layout=%d is not a pi_rope_layout", d->layout);
+  if (d->scaling < PI_ROPE_NONE || d->scaling > PI_ROPE_BANDS)
+    return fail(PI_ERR_INVALID, "scaling=%d is not a pi_rope_scaling", d->scaling);
+  if (!(d->gain > 0) || !std::isfinite((float)d->gain)) return fail(PI_ERR_INVALID, "gain=%g must be positive and finite", d->gain);
+  if (d->freqs != nullptr) {
+    if (d->scaling != PI_ROPE_NONE) return fail(PI_ERR_INVALID, "freqs are given: scaling must be PI_ROPE_NONE");
+    for (int i = 0; i < d->rot_dims / 2; ++i)
+      if (!(d->freqs[i] >= 0 && d->freqs[i] <= kPi))
+        return fail(PI_ERR_INVALID, "freqs[%d]=%g must lie in [0, pi]", i, d->freqs[i]);
+    return PI_OK;
+  }
+  if (!(d->base >= 1) || !std::isfinite(d->base)) return fail(PI_ERR_INVALID, "base=%g must be at least 1", d->base);
+  if (d->scaling != PI_ROPE_NONE && (!(d->factor >= 1) || !std::isfinite(d->factor)))
+    return fail(PI_ERR_INVALID, "factor=%g must be at least 1", d->factor);
+  if (d->scaling == PI_ROPE_BANDS && (!(d->original > 0) || !std::isfinite(d->original) || !(d->low >= 0) ||
+                                      !(d->high > d->low) || !std::isfinite(d->high)))
+    return fail(PI_ERR_INVALID, "original=%g must be positive and 0 <= low=%g < high=%g", d->original, d->low, d->high);
+  return PI_OK;
+}
+
+// f_i as pi_kv.h defines it.
+double rope_freq(const pi_rope_desc& d, int i) {
+  if (d.freqs != nullptr) return d.freqs[i];
+  const double n = d.rot_dims, base = d.scaling == PI_ROPE_NTK ? d.base * std::pow(d.factor, n / (n - 2)) : d.base;
+  const double f = std::pow(base, -2.0 * i / n);
+  if (d.scaling == PI_ROPE_LINEAR) return f / d.factor;
+  if (d.scaling != PI_ROPE_BANDS) return f;
+  const double keep = std::min(std::max((d.original * f / (2 * kPi) - d.low) / (d.high - d.low), 0.0), 1.0);
+  return keep * f + (1 - keep) * f / d.factor;
+}
 
 pik::KvView view_of(const pi_kv* h, int layer, const pi_kv_batch* b) {
   const pi_kv_desc& d = h->desc;
@@ -280,6 +328,69 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
   if (counts && shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32))
     return launched(pik::launch_kv_step(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
   return launched(pik::launch_kv_tile(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
+}
+
+pi_status pi_rope_create(const pi_rope_desc* desc, pi_rope** out) {
+  if (out == nullptr) return fail(PI_ERR_INVALID, "out is NULL");
+  *out = nullptr;
+  const pi_status st = check_rope(desc);
+  if (st != PI_OK) return st;
+  pi_rope* r = new (std::nothrow) pi_rope{};
+  if (r == nullptr) return fail(PI_ERR_INVALID, "out of host memory");
+  r->desc = *desc;
+  r->desc.freqs = nullptr;
+  for (int i = 0; i < desc->rot_dims / 2; ++i) {
+    r->freqs[i] = rope_freq(*desc, i);
+    r->turns[i] = (uint64_t)((long double)r->freqs[i] / 6.283185307179586476925286766559006L * 0x1p64L + 0.5L);
+  }
+  *out = r;
+  return ok();
+}
+
+pi_status pi_rope_destroy(pi_rope* rope) {
+  if (rope == nullptr) return fail(PI_ERR_INVALID, "rope is NULL");
+  delete rope;
+  return ok();
+}
+
+pi_status pi_rope_freqs(const pi_rope* rope, double* freqs) {
+  if (rope == nullptr || freqs == nullptr) return fail(PI_ERR_INVALID, "rope or freqs is NULL");
+  for (int i = 0; i < rope->desc.rot_dims / 2; ++i) freqs[i] = rope->freqs[i];
+  return ok();
+}
+
+pi_status pi_kv_rotate(pi_kv* h, const pi_rope* rope, const pi_kv_rotate_args* args, const pi_kv_batch* batch,
+                       void* stream) {
+  pi_status st = check_batch(h, 0, batch);
+  if (st != PI_OK) return st;
+  if (rope == nullptr) return fail(PI_ERR_INVALID, "rope is NULL");
+  if (args == nullptr) return fail(PI_ERR_INVALID, "args is NULL");
+  if (rope->desc.head_dim != h->desc.head_dim)
+    return fail(PI_ERR_INVALID, "the rope's head_dim=%d is not the cache's %d", rope->desc.head_dim, h->desc.head_dim);
+  if ((args->q_norm != nullptr || args->k_norm != nullptr) && (!(args->eps > 0.0f) || !std::isfinite(args->eps)))
+    return fail(PI_ERR_INVALID, "eps=%g must be positive and finite", (double)args->eps);
+  if (!aligned(args->q_norm, 16) || !aligned(args->k_norm, 16))
+    return fail(PI_ERR_INVALID, "q_norm or k_norm is not 16-byte aligned");
+  if (!aligned(args->positions, 4)) return fail(PI_ERR_INVALID, "positions is not 4-byte aligned");
+  if (batch->rows == 0) return ok();
+  if ((st = check_rows(&args->q, "q")) != PI_OK || (st = check_rows(&args->q_out, "q_out")) != PI_OK ||
+      (st = check_rows(&args->k, "k")) != PI_OK || (st = check_rows(&args->k_out, "k_out")) != PI_OK)
+    return st;
+  pik::KvRotateArgs a{};
+  a.c = view_of(h, 0, batch);
+  a.q = rows_of(&args->q);
+  a.q_out = rows_of(&args->q_out);
+  a.k = rows_of(&args->k);
+  a.k_out = rows_of(&args->k_out);
+  a.q_norm = args->q_norm;
+  a.k_norm = args->k_norm;
+  a.positions = args->positions;
+  a.heads = h->desc.heads;
+  a.rot = rope->desc.rot_dims;
+  a.eps = args->eps;
+  a.gain = (float)rope->desc.gain;
+  std::copy(rope->turns, rope->turns + pik::kMaxPairs, a.turns);
+  return launched(pik::launch_kv_rotate(h->desc.act_dtype, rope->desc.layout, a, static_cast<hipStream_t>(stream)), "rotate");
 }
 
 pi_status pi_kv_reserve(pi_kv* h, const int32_t* seqs, const int32_t* counts, int32_t n, void* stream) {

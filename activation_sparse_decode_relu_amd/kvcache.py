@@ -16,14 +16,17 @@ from .binding import LIB, PI_ERR_INVALID, PiError, _invalid, check
 PI_KV_F16, PI_KV_BF16 = range(2)
 PI_KV_E4M3, PI_KV_INT8 = range(2)
 KV_BLOCK = 32
-KV_ABI_VERSION = 2   # PI_KV_ABI_VERSION of the header this binding follows
+KV_ABI_VERSION = 3   # PI_KV_ABI_VERSION of the header this binding follows
 
 ACTS = {"f16": PI_KV_F16, "bf16": PI_KV_BF16}
 CODES = {"e4m3": PI_KV_E4M3, "int8": PI_KV_INT8}
 _ACT_TORCH = {PI_KV_F16: torch.float16, PI_KV_BF16: torch.bfloat16}
 
 KV_EXPORTED = ("pi_kv_abi_version", "pi_kv_workspace_bytes", "pi_kv_create", "pi_kv_destroy", "pi_kv_append",
-               "pi_kv_read", "pi_kv_attend", "pi_kv_reserve", "pi_kv_free", "pi_kv_fork", "pi_kv_compact")
+               "pi_kv_read", "pi_kv_attend", "pi_kv_reserve", "pi_kv_free", "pi_kv_fork", "pi_kv_compact", "pi_kv_rotate")
+ROPE_EXPORTED = ("pi_rope_create", "pi_rope_destroy", "pi_rope_freqs")
+LAYOUTS = {"half": 0, "interleaved": 1}
+SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -53,6 +56,17 @@ class KvAttendArgs(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = ([(name, _i32) for name in ("head_dim", "rot_dims", "layout", "scaling")] +
+                [(name, ctypes.c_double) for name in ("base", "factor", "original", "low", "high", "gain")] +
+                [("freqs", ctypes.POINTER(ctypes.c_double))])
+
+
+class KvRotateArgs(ctypes.Structure):
+    _fields_ = [("q", KvRows), ("q_out", KvRows), ("k", KvRows), ("k_out", KvRows), ("q_norm", _vp), ("k_norm", _vp),
+                ("positions", _vp), ("eps", ctypes.c_float)]
+
+
 def _declare() -> None:
     p = ctypes.POINTER
     sigs = dict(pi_kv_workspace_bytes=[p(KvDesc), p(ctypes.c_size_t)],
@@ -64,7 +78,11 @@ def _declare() -> None:
                 pi_kv_reserve=[_vp, _vp, _vp, _i32, _vp],
                 pi_kv_free=[_vp, _vp, _i32, _vp],
                 pi_kv_fork=[_vp, _vp, _vp, _i32, _vp],
-                pi_kv_compact=[_vp, _vp])
+                pi_kv_compact=[_vp, _vp],
+                pi_kv_rotate=[_vp, _vp, p(KvRotateArgs), p(KvBatch), _vp],
+                pi_rope_create=[p(RopeDesc), p(_vp)],
+                pi_rope_destroy=[_vp],
+                pi_rope_freqs=[_vp, p(ctypes.c_double)])
     for name, args in sigs.items():
         fn = getattr(LIB, name)
         fn.restype, fn.argtypes = ctypes.c_int, args
@@ -103,8 +121,48 @@ def kv_workspace_bytes(desc: KvDesc) -> int:
     return int(out.value)
 
 
+class Rope:
+    """The rotation of a head's first rot_dims dims (all of them unless given) by position, for KVCache.rotate.
+
+    Pair i turns by base^(-2 i / rot_dims) a position; layout "half" pairs dims i and i + rot_dims / 2, "interleaved"
+    2 i and 2 i + 1.  For contexts longer than the trained ones the frequencies are scaled by `factor`: "linear" (all of
+    them), "ntk" (a larger base), "bands" (by the turns a pair makes within the `original` length: none of it from
+    `high` turns on, all of it up to `low`; pi_kv.h has the formulas).  `gain` multiplies cosines and sines.  `freqs`
+    (rot_dims / 2 numbers, radians a position) takes the place of base and scaling.  Host memory only.
+    """
+
+    def __init__(self, head_dim, rot_dims=None, layout="half", base=10000.0, scaling="none", factor=1.0, original=0.0,
+                 low=1.0, high=32.0, gain=1.0, freqs=None):
+        self.handle = None
+        whole = dict(head_dim=head_dim, rot_dims=head_dim if rot_dims is None else rot_dims,
+                     layout=LAYOUTS[layout] if isinstance(layout, str) else layout,
+                     scaling=SCALINGS[scaling] if isinstance(scaling, str) else scaling)
+        whole = {name: int(value) for name, value in whole.items()}
+        _in32(**whole)
+        self.desc = d = RopeDesc(*whole.values(), base, factor, original, low, high, gain, None)
+        if freqs is not None:
+            freqs = [float(f) for f in freqs]
+            if len(freqs) != d.rot_dims // 2:
+                raise _invalid(f"freqs must have rot_dims / 2 = {d.rot_dims // 2} entries, got {len(freqs)}")
+            d.freqs = (ctypes.c_double * len(freqs))(*freqs)
+        handle = _vp()
+        check(LIB.pi_rope_create(_byref(d), _byref(handle)))
+        self.handle = handle
+
+    def freqs(self) -> list:
+        """The frequencies as scaled, in radians a position."""
+        out = (ctypes.c_double * max(self.desc.rot_dims // 2, 1))()
+        check(LIB.pi_rope_freqs(self.handle, out))
+        return list(out)[:self.desc.rot_dims // 2]
+
+    def __del__(self):
+        if getattr(self, "handle", None) is not None and self.handle.value:
+            LIB.pi_rope_destroy(self.handle)
+            self.handle = None
+
+
 class KVCache:
-    """A paged cache of keys and values in 8-bit codes, and the attention that reads it.
+    """A paged cache of keys and values in 8-bit codes, the attention that reads it, and what brings queries and keys there.
 
     One object holds every layer's pages; the table, the lengths and the reference counts are shared by
     the layers.  All of them are device tensors that the caller may read or set between calls:
@@ -329,6 +387,39 @@ class KVCache:
         batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
         self._run(LIB.pi_kv_attend, self._live(), layer, _byref(args), _byref(batch),
                   self._stream(stream, (q, out, seqs, starts, lse)))
+
+    def rotate(self, rope, q, q_out, k, k_out, seqs, starts, positions=None, q_norm=None, k_norm=None, eps=1e-6,
+               stream=None) -> None:
+        """Queries [rows][heads][head_dim] and keys [rows][kv_heads][head_dim] as append and attend take them: each head
+        divided by its root mean square and times q_norm or k_norm ([head_dim] of the activations' type), where that is
+        given; then turned by its token's position as `rope` says: row starts[i] + j of seqs[i] is token
+        lens[seqs[i]] - count + j (reserve has counted it), or positions[row] (int32).  Outputs may be the inputs
+        themselves."""
+        if not isinstance(rope, Rope):
+            raise _invalid(f"rope must be a Rope, not {type(rope).__name__}")
+        d = self.desc
+        n = self._ids(seqs, "seqs")
+        self._ids(starts, "starts", n + 1)
+        qr = self._rows(q, "q", d.heads)
+        rows = q.shape[0]
+        kr = self._rows(k, "k", d.kv_heads, rows)
+        qo = qr if q_out is q else self._rows(q_out, "q_out", d.heads, rows)
+        ko = kr if k_out is k else self._rows(k_out, "k_out", d.kv_heads, rows)
+        self._writable(q_out, "q_out")
+        self._writable(k_out, "k_out")
+        for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if t is not None:
+                self._dense(t, name, self._act, (d.head_dim,))
+        if positions is not None:
+            self._ids(positions, "positions", rows)
+        if rows >> 31:
+            _in32(rows=rows)
+        args = KvRotateArgs(qr, qo, kr, ko, None if q_norm is None else q_norm.data_ptr(),
+                            None if k_norm is None else k_norm.data_ptr(),
+                            None if positions is None else positions.data_ptr(), eps)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
+        self._run(LIB.pi_kv_rotate, self._live(), rope.handle, _byref(args), _byref(batch),
+                  self._stream(stream, (q, q_out, k, k_out, seqs, starts, positions, q_norm, k_norm)))
 
     # ---- pages ------------------------------------------------------------------------------------
 

@@ -8,6 +8,7 @@
  *   attend   out = softmax(scale q K^T + mask) V for one token a sequence, a few, or whole prompts
  *   read     the stored keys and values, back in the activations' type
  *   reserve, free, fork, compact   move the pages; a page may belong to several sequences
+ *   rotate   norms of queries and keys for each head, and their rotation by position, before append and attend
  *
  * What is stored
  * --------------
@@ -58,7 +59,7 @@
 extern "C" {
 #endif
 
-#define PI_KV_ABI_VERSION 2
+#define PI_KV_ABI_VERSION 3
 
 #define PI_KV_BLOCK 32 /* tokens that share an exponent */
 
@@ -113,6 +114,47 @@ typedef struct pi_kv_attend_args {
   int32_t sinks;   /* with a window: first tokens that every later row sees too   */
   float scale;     /* positive and finite                                         */
 } pi_kv_attend_args;
+
+/*
+ * The rotation of a head's first rot_dims dims by position.  Pair i of them turns by p * f_i at position p:
+ *   (a, b) -> gain * (a cos t - b sin t, a sin t + b cos t),   t = p f_i,
+ * with f_i = base^(-2 i / rot_dims), scaled for contexts longer than those a model was trained on.
+ */
+typedef enum pi_rope_layout {
+  PI_ROPE_HALF = 0,       /* pair i: dims i and i + rot_dims / 2 */
+  PI_ROPE_INTERLEAVED = 1 /* pair i: dims 2 i and 2 i + 1        */
+} pi_rope_layout;
+typedef enum pi_rope_scaling {
+  PI_ROPE_NONE = 0,
+  PI_ROPE_LINEAR = 1, /* f_i / factor                                                              */
+  PI_ROPE_NTK = 2,    /* base * factor^(rot_dims / (rot_dims - 2)) in the place of base            */
+  PI_ROPE_BANDS = 3   /* by the turns r = original f_i / (2 pi) a pair makes within the original length:
+                         f_i where r >= high, f_i / factor where r <= low, and in between
+                         k f_i + (1 - k) f_i / factor, k = (r - low) / (high - low)                  */
+} pi_rope_scaling;
+typedef struct pi_rope_desc {
+  int32_t head_dim;    /* D: 64 or 128                                               */
+  int32_t rot_dims;    /* a multiple of 16 up to D, 0 for none (norms alone)         */
+  int32_t layout;      /* pi_rope_layout                                             */
+  int32_t scaling;     /* pi_rope_scaling                                            */
+  double base;         /* at least 1                                                 */
+  double factor;       /* at least 1                                                 */
+  double original;     /* PI_ROPE_BANDS: tokens, positive                            */
+  double low, high;    /* PI_ROPE_BANDS: 0 <= low < high                             */
+  double gain;         /* factor of the cosines and sines, positive; 1 for none      */
+  const double* freqs; /* host, [rot_dims / 2], each in [0, pi]: f_i itself, in the place of base and scaling; or NULL */
+} pi_rope_desc;
+typedef struct pi_rope pi_rope;
+
+/* Outputs may be the inputs themselves, and overlap them in no other way. */
+typedef struct pi_kv_rotate_args {
+  pi_kv_rows q, q_out;      /* [rows][heads][D]                                              */
+  pi_kv_rows k, k_out;      /* [rows][kv_heads][D]                                           */
+  const void* q_norm;       /* [D] of the activations' type, 16-byte aligned, or NULL        */
+  const void* k_norm;
+  const int32_t* positions; /* [rows], or NULL: those of the batch's tokens                  */
+  float eps;                /* positive and finite (looked at with a norm)                   */
+} pi_kv_rotate_args;
 
 typedef struct pi_kv pi_kv;
 
@@ -176,6 +218,21 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
  * these is counted in `failed` and, unless it asked for 0 tokens, marked in `refused`.
  */
 pi_status pi_kv_reserve(pi_kv* h, const int32_t* seqs, const int32_t* counts, int32_t n, void* stream);
+
+/* Work the frequencies out (host only; a rope has no device memory) and release them. */
+pi_status pi_rope_create(const pi_rope_desc* desc, pi_rope** out);
+pi_status pi_rope_destroy(pi_rope* rope);
+/* The frequencies f_i [rot_dims / 2], as scaled, in radians a position.  Host only. */
+pi_status pi_rope_freqs(const pi_rope* rope, double* freqs);
+
+/*
+ * Queries and keys as append and attend take them: with a norm, each head x becomes x / sqrt(mean x^2 + eps) * norm;
+ * then its first dims turn by their token's position, lens[s] - count + j for row starts[i] + j of s = seqs[i], as in
+ * pi_kv_attend (lens counts the tokens already), or the given one.  In fp32 (a head's sum of squares has to be in
+ * its range), rounded once; angles are exact to 2^-32 of a turn at any position.  Rows of no sequence stay as they are.
+ */
+pi_status pi_kv_rotate(pi_kv* h, const pi_rope* rope, const pi_kv_rotate_args* args, const pi_kv_batch* batch,
+                       void* stream);
 
 /* Drop the sequences' pages: refs of each goes down by one, table rows become -1, lens 0. */
 pi_status pi_kv_free(pi_kv* h, const int32_t* seqs, int32_t n, void* stream);
