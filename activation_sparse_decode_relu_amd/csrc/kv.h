@@ -51,6 +51,26 @@ struct KvAttendArgs {
   unsigned* tickets;   // workspace: kStepTickets counters, zero between calls
 };
 
+// What a call of the attention kernels takes: whole sequences; the tokens that the sequences of a group share, for all
+// rows of the group (an item is a group, max_new its rows), whose states are left in `state`; or what each sequence
+// holds behind these, joined with the states.
+enum : int { ATTEND_ALL = 0, ATTEND_SHARED = 1, ATTEND_OWN = 2 };
+struct KvSharedArgs : KvAttendArgs {
+  const int* groups;   // [n_groups + 1]: group g is the sequences groups[g] .. groups[g + 1] of the call
+  const int* plan;     // [n_groups + n]: shared tokens of each group, and of each sequence's group
+  float* state;        // [rows][heads][D + 4]: O' and rr, mm, l (kv_softmax.h)
+  int n_groups;
+};
+struct KvShareArgs {
+  KvView c;
+  const int* groups;
+  int* plan;
+  int n_groups;
+};
+hipError_t launch_kv_share(const KvShareArgs& a, hipStream_t s);
+hipError_t launch_kv_step_shared(int act, int code, int mode, const KvSharedArgs& a, hipStream_t s);
+hipError_t launch_kv_tile_shared(int act, int code, int mode, const KvSharedArgs& a, hipStream_t s);
+
 // Few rows of a cached head (max_new * group up to kStepRows): items (sequences times cached heads) in pieces, one
 // workgroup each, see kv_step.hip.  S is at least kStepGrain blocks.
 constexpr int kStepRows = 64, kStepGrain = 8;

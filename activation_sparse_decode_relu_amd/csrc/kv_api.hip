@@ -209,6 +209,62 @@ pi_status check_rows(const pi_kv_rows* t, const char* name) {
 
 pik::KvRows rows_of(const pi_kv_rows* t) { return pik::KvRows{t->data, t->token_stride, t->head_stride}; }
 
+pi_status check_attend(const pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_batch* batch) {
+  pi_status st = check_batch(h, layer, batch);
+  if (st != PI_OK) return st;
+  if (args == nullptr) return fail(PI_ERR_INVALID, "args is NULL");
+  if (args->window < 0 || args->sinks < 0)
+    return fail(PI_ERR_INVALID, "window=%d and sinks=%d must not be negative", args->window, args->sinks);
+  if (!(args->scale > 0.0f) || !std::isfinite(args->scale))
+    return fail(PI_ERR_INVALID, "scale=%g must be positive and finite", (double)args->scale);
+  if (batch->rows == 0) return ok();
+  if (args->max_new < 1 || args->max_new > batch->rows)
+    return fail(PI_ERR_INVALID, "max_new=%d must lie in [1, rows=%d]", args->max_new, batch->rows);
+  if ((st = check_rows(&args->q, "q")) != PI_OK || (st = check_rows(&args->out, "out")) != PI_OK) return st;
+  if (!aligned(args->lse, 4)) return fail(PI_ERR_INVALID, "lse is not 4-byte aligned");
+  return PI_OK;
+}
+
+pi_status check_groups(const pi_kv_batch* b, const int32_t* groups, int32_t n_groups) {
+  if (n_groups < 1 || n_groups > b->n) return fail(PI_ERR_INVALID, "n_groups=%d must lie in [1, n=%d]", n_groups, b->n);
+  return check_ints(groups, "groups");
+}
+
+size_t state_bytes(const pi_kv_desc& d, int32_t rows) {
+  return (size_t)rows * d.heads * (d.head_dim + 4) * sizeof(float);
+}
+
+void fill_attend(pik::KvAttendArgs& a, const pi_kv* h, int32_t layer, const pi_kv_attend_args* args,
+                 const pi_kv_batch* batch) {
+  a.c = view_of(h, layer, batch);
+  a.q = rows_of(&args->q);
+  a.out = rows_of(&args->out);
+  a.lse = args->lse;
+  a.heads = h->desc.heads;
+  a.group = h->desc.heads / h->desc.kv_heads;
+  a.max_new = args->max_new;
+  a.window = args->window;
+  a.sinks = args->sinks;
+  a.scale = args->scale;
+  a.partial = reinterpret_cast<float*>(h->ws + h->L.partial);
+  a.tickets = reinterpret_cast<unsigned*>(h->ws + h->L.tickets);
+}
+
+// Rows of a cached head for which the codes go straight to the matrix instructions; more go through LDS.  33 to 64
+// rows of 128 dims are slow there (one workgroup a compute unit, and large parts to join), which pays only where
+// there are items enough: eight tokens on one head of eight query heads, sequences of 4000, took 34.9 us against
+// 24.1 through LDS with 16 items, 36.4 against 31.1 with 32, 41.2 against 41.8 with 64 and 56 against 82 with 128.
+// With 64 dims, four tokens of 16 query heads, 48.6 against 62.7 us over 100003 tokens, 18.1 against 14.2 over 2000.
+// That kernel counts the call's blocks of 32 tokens in 32 bits: a table with room for more (2^30 tokens each of eight
+// sequences on eight heads, say) goes through LDS, whatever it holds.  `most` rows of an item, `count` items.
+bool few_rows(const pik::KvAttendArgs& a, int most, int count) {
+  const int64_t shared = (int64_t)most * a.group, items = (int64_t)count * a.c.kv_heads;
+  const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
+  const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + most) / PI_KV_BLOCK + 4) : cap;
+  const bool counts = (seen + pik::kStepGrain) * items <= INT32_MAX;
+  return counts && shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32);
+}
+
 pi_status launched(hipError_t e, const char* what) {
   if (e != hipSuccess) return fail(PI_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(e));
   return ok();
@@ -289,45 +345,63 @@ pi_status pi_kv_read(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_r
 }
 
 pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_batch* batch, void* stream) {
-  pi_status st = check_batch(h, layer, batch);
-  if (st != PI_OK) return st;
-  if (args == nullptr) return fail(PI_ERR_INVALID, "args is NULL");
-  if (args->window < 0 || args->sinks < 0)
-    return fail(PI_ERR_INVALID, "window=%d and sinks=%d must not be negative", args->window, args->sinks);
-  if (!(args->scale > 0.0f) || !std::isfinite(args->scale))
-    return fail(PI_ERR_INVALID, "scale=%g must be positive and finite", (double)args->scale);
-  if (batch->rows == 0) return ok();
-  if (args->max_new < 1 || args->max_new > batch->rows)
-    return fail(PI_ERR_INVALID, "max_new=%d must lie in [1, rows=%d]", args->max_new, batch->rows);
-  if ((st = check_rows(&args->q, "q")) != PI_OK || (st = check_rows(&args->out, "out")) != PI_OK) return st;
-  if (!aligned(args->lse, 4)) return fail(PI_ERR_INVALID, "lse is not 4-byte aligned");
+  pi_status st = check_attend(h, layer, args, batch);
+  if (st != PI_OK || batch->rows == 0) return st;
   pik::KvAttendArgs a{};
-  a.c = view_of(h, layer, batch);
-  a.q = rows_of(&args->q);
-  a.out = rows_of(&args->out);
-  a.lse = args->lse;
-  a.heads = h->desc.heads;
-  a.group = h->desc.heads / h->desc.kv_heads;
-  a.max_new = args->max_new;
-  a.window = args->window;
-  a.sinks = args->sinks;
-  a.scale = args->scale;
-  a.partial = reinterpret_cast<float*>(h->ws + h->L.partial);
-  a.tickets = reinterpret_cast<unsigned*>(h->ws + h->L.tickets);
-  // Rows of a cached head for which the codes go straight to the matrix instructions; more go through LDS.  33 to 64
-  // rows of 128 dims are slow there (one workgroup a compute unit, and large parts to join), which pays only where
-  // there are items enough: eight tokens on one head of eight query heads, sequences of 4000, took 34.9 us against
-  // 24.1 through LDS with 16 items, 36.4 against 31.1 with 32, 41.2 against 41.8 with 64 and 56 against 82 with 128.
-  // With 64 dims, four tokens of 16 query heads, 48.6 against 62.7 us over 100003 tokens, 18.1 against 14.2 over 2000.
-  // That kernel counts the call's blocks of 32 tokens in 32 bits: a table with room for more (2^30 tokens each of eight
-  // sequences on eight heads, say) goes through LDS, whatever it holds.
-  const int64_t shared = (int64_t)a.max_new * a.group, items = (int64_t)a.c.n * a.c.kv_heads;
-  const int64_t cap = (int64_t)a.c.max_pages * a.c.page_blocks;
-  const int64_t seen = a.window > 0 ? std::min(cap, ((int64_t)a.window + a.sinks + a.max_new) / PI_KV_BLOCK + 4) : cap;
-  const bool counts = (seen + pik::kStepGrain) * items <= INT32_MAX;
-  if (counts && shared <= (a.c.dim == 64 || items >= 64 ? pik::kStepRows : 32))
-    return launched(pik::launch_kv_step(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
-  return launched(pik::launch_kv_tile(h->desc.act_dtype, h->desc.code, a, static_cast<hipStream_t>(stream)), "attend");
+  fill_attend(a, h, layer, args, batch);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (few_rows(a, a.max_new, a.c.n)) return launched(pik::launch_kv_step(h->desc.act_dtype, h->desc.code, a, s), "attend");
+  return launched(pik::launch_kv_tile(h->desc.act_dtype, h->desc.code, a, s), "attend");
+}
+
+pi_status pi_kv_share(pi_kv* h, const pi_kv_batch* batch, const int32_t* groups, int32_t n_groups, int32_t* plan,
+                      void* stream) {
+  pi_status st = check_batch(h, 0, batch);
+  if (st != PI_OK) return st;
+  if ((st = check_groups(batch, groups, n_groups)) != PI_OK || (st = check_ints(plan, "plan")) != PI_OK) return st;
+  pik::KvShareArgs a{view_of(h, 0, batch), groups, plan, n_groups};
+  return launched(pik::launch_kv_share(a, static_cast<hipStream_t>(stream)), "share");
+}
+
+pi_status pi_kv_state_bytes(const pi_kv* h, int32_t rows, size_t* bytes) {
+  if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
+  if (bytes == nullptr) return fail(PI_ERR_INVALID, "bytes is NULL");
+  if (rows < 0 || rows > kMaxRows) return fail(PI_ERR_INVALID, "rows=%d must lie in [0, %d]", rows, kMaxRows);
+  *bytes = state_bytes(h->desc, rows);
+  return ok();
+}
+
+pi_status pi_kv_attend_shared(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_shared_args* shared,
+                              const pi_kv_batch* batch, void* stream) {
+  pi_status st = check_attend(h, layer, args, batch);
+  if (st != PI_OK) return st;
+  if (shared == nullptr) return fail(PI_ERR_INVALID, "shared is NULL");
+  if (args->window != 0 || args->sinks != 0)
+    return fail(PI_ERR_UNSUPPORTED, "window=%d, sinks=%d: shared tokens are attended over as a whole", args->window, args->sinks);
+  if ((st = check_groups(batch, shared->groups, shared->n_groups)) != PI_OK ||
+      (st = check_ints(shared->plan, "plan")) != PI_OK)
+    return st;
+  if (batch->rows == 0) return ok();
+  if (shared->max_rows < 1 || shared->max_rows > batch->rows)
+    return fail(PI_ERR_INVALID, "max_rows=%d must lie in [1, rows=%d]", shared->max_rows, batch->rows);
+  const size_t need = state_bytes(h->desc, batch->rows);
+  if (shared->state == nullptr || !aligned(shared->state, 16) || shared->state_bytes < need)
+    return fail(PI_ERR_WORKSPACE, "state must be %zu bytes, 16-byte aligned", need);
+  pik::KvSharedArgs a{};
+  fill_attend(a, h, layer, args, batch);
+  a.groups = shared->groups;
+  a.plan = shared->plan;
+  a.state = static_cast<float*>(shared->state);
+  a.n_groups = shared->n_groups;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  for (int mode : {pik::ATTEND_SHARED, pik::ATTEND_OWN}) {
+    a.max_new = mode == pik::ATTEND_SHARED ? shared->max_rows : args->max_new;
+    const bool few = few_rows(a, a.max_new, mode == pik::ATTEND_SHARED ? a.n_groups : a.c.n);
+    const hipError_t e = few ? pik::launch_kv_step_shared(h->desc.act_dtype, h->desc.code, mode, a, s)
+                             : pik::launch_kv_tile_shared(h->desc.act_dtype, h->desc.code, mode, a, s);
+    if (e != hipSuccess) return launched(e, "attend_shared");
+  }
+  return ok();
 }
 
 pi_status pi_rope_create(const pi_rope_desc* desc, pi_rope** out) {

@@ -23,7 +23,8 @@ CODES = {"e4m3": PI_KV_E4M3, "int8": PI_KV_INT8}
 _ACT_TORCH = {PI_KV_F16: torch.float16, PI_KV_BF16: torch.bfloat16}
 
 KV_EXPORTED = ("pi_kv_abi_version", "pi_kv_workspace_bytes", "pi_kv_create", "pi_kv_destroy", "pi_kv_append",
-               "pi_kv_read", "pi_kv_attend", "pi_kv_reserve", "pi_kv_free", "pi_kv_fork", "pi_kv_compact", "pi_kv_rotate")
+               "pi_kv_read", "pi_kv_attend", "pi_kv_reserve", "pi_kv_free", "pi_kv_fork", "pi_kv_compact", "pi_kv_rotate",
+               "pi_kv_share", "pi_kv_state_bytes", "pi_kv_attend_shared")
 ROPE_EXPORTED = ("pi_rope_create", "pi_rope_destroy", "pi_rope_freqs")
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3}
@@ -67,6 +68,11 @@ class KvRotateArgs(ctypes.Structure):
                 ("positions", _vp), ("eps", ctypes.c_float)]
 
 
+class KvSharedArgs(ctypes.Structure):
+    _fields_ = [("groups", _vp), ("plan", _vp), ("state", _vp), ("state_bytes", ctypes.c_size_t), ("n_groups", _i32),
+                ("max_rows", _i32)]
+
+
 def _declare() -> None:
     p = ctypes.POINTER
     sigs = dict(pi_kv_workspace_bytes=[p(KvDesc), p(ctypes.c_size_t)],
@@ -80,6 +86,9 @@ def _declare() -> None:
                 pi_kv_fork=[_vp, _vp, _vp, _i32, _vp],
                 pi_kv_compact=[_vp, _vp],
                 pi_kv_rotate=[_vp, _vp, p(KvRotateArgs), p(KvBatch), _vp],
+                pi_kv_share=[_vp, p(KvBatch), _vp, _i32, _vp, _vp],
+                pi_kv_state_bytes=[_vp, _i32, p(ctypes.c_size_t)],
+                pi_kv_attend_shared=[_vp, _i32, p(KvAttendArgs), p(KvSharedArgs), p(KvBatch), _vp],
                 pi_rope_create=[p(RopeDesc), p(_vp)],
                 pi_rope_destroy=[_vp],
                 pi_rope_freqs=[_vp, p(ctypes.c_double)])
@@ -387,6 +396,61 @@ class KVCache:
         batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
         self._run(LIB.pi_kv_attend, self._live(), layer, _byref(args), _byref(batch),
                   self._stream(stream, (q, out, seqs, starts, lse)))
+
+    def _groups(self, groups, plan, n) -> int:
+        """Check groups and plan for n sequences; returns the number of groups."""
+        count = self._ids(groups, "groups") - 1
+        if not 1 <= count <= n:
+            raise _invalid(f"groups must have 2 to {n + 1} entries, got {count + 1}")
+        self._ids(plan, "plan", count + n)
+        return count
+
+    def share(self, seqs, starts, groups, plan, stream=None) -> None:
+        """How much the sequences of each group share: group g is seqs[groups[g]:groups[g + 1]] (groups int32, ascending
+        from 0 to len(seqs)), and plan (int32 [groups + sequences]) gets, for each group and then for each sequence, the
+        number of leading tokens whose pages the whole group names alike, among those held before this call's rows.
+        Once a step is enough for all layers: a plan holds until lengths or pages change."""
+        n = self._ids(seqs, "seqs")
+        self._ids(starts, "starts", n + 1)
+        count = self._groups(groups, plan, n)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, (1 << 24))   # starts alone say which rows there are
+        self._run(LIB.pi_kv_share, self._live(), _byref(batch), groups.data_ptr(), count, plan.data_ptr(),
+                  self._stream(stream, (seqs, starts, groups, plan)))
+
+    def attend_shared(self, layer, q, out, seqs, starts, groups, plan, max_new, max_rows, scale=None, lse=None, state=None,
+                      stream=None) -> None:
+        """attend (whole sequences, no window) for groups of sequences that begin with the same pages: what `plan` (share)
+        says a group shares is read and multiplied once for all of its rows.  max_rows: at least the largest count of
+        rows of a group.  state: fp32 scratch of rows * heads * (head_dim + 4) elements, made here unless given."""
+        d = self.desc
+        n = self._ids(seqs, "seqs")
+        self._ids(starts, "starts", n + 1)
+        count = self._groups(groups, plan, n)
+        qr = self._rows(q, "q", d.heads)
+        rows = q.shape[0]
+        orow = self._rows(out, "out", d.heads, rows)
+        self._writable(out, "out")
+        if lse is not None:
+            self._dense(lse, "lse", torch.float32, (rows, d.heads))
+        if (layer | rows | max_new | max_rows) >> 31:
+            _in32(layer=layer, rows=rows, max_new=max_new, max_rows=max_rows)
+        handle = self._live()
+        if state is None:
+            size = rows * d.heads * (d.head_dim + 4)
+            if stream is None:
+                state = torch.empty(size, dtype=torch.float32, device=self.device)
+            else:   # of the stream that uses it
+                with torch.cuda.stream(stream):
+                    state = torch.empty(size, dtype=torch.float32, device=self.device)
+        if not isinstance(state, torch.Tensor) or state.device != self.device or state.dtype is not torch.float32 or \
+                not state.is_contiguous():
+            raise _invalid(f"state must be a contiguous torch.float32 tensor on {self.device}")
+        args = KvAttendArgs(qr, orow, None if lse is None else lse.data_ptr(), max_new, 0, 0,
+                            d.head_dim ** -0.5 if scale is None else scale)
+        more = KvSharedArgs(groups.data_ptr(), plan.data_ptr(), state.data_ptr(), state.numel() * 4, count, max_rows)
+        batch = KvBatch(seqs.data_ptr(), starts.data_ptr(), n, rows)
+        self._run(LIB.pi_kv_attend_shared, handle, layer, _byref(args), _byref(more), _byref(batch),
+                  self._stream(stream, (q, out, seqs, starts, groups, plan, lse, state)))
 
     def rotate(self, rope, q, q_out, k, k_out, seqs, starts, positions=None, q_norm=None, k_norm=None, eps=1e-6,
                stream=None) -> None:

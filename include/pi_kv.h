@@ -6,6 +6,7 @@
  *
  *   append   store the last tokens of each sequence
  *   attend   out = softmax(scale q K^T + mask) V for one token a sequence, a few, or whole prompts
+ *   share, attend_shared   the same for sequences that begin with the same pages, read and multiplied once for all
  *   read     the stored keys and values, back in the activations' type
  *   reserve, free, fork, compact   move the pages; a page may belong to several sequences
  *   rotate   norms of queries and keys for each head, and their rotation by position, before append and attend
@@ -156,6 +157,19 @@ typedef struct pi_kv_rotate_args {
   float eps;                /* positive and finite (looked at with a norm)                   */
 } pi_kv_rotate_args;
 
+/*
+ * Groups of a call's sequences that begin with the same pages (forks of one prompt): group g is the sequences
+ * seqs[groups[g]] .. seqs[groups[g + 1] - 1], groups ascending from 0 to n.
+ */
+typedef struct pi_kv_shared_args {
+  const int32_t* groups; /* [n_groups + 1]                                                     */
+  const int32_t* plan;   /* [n_groups + n], as pi_kv_share leaves it                           */
+  void* state;           /* scratch of the call: pi_kv_state_bytes, 16-byte aligned            */
+  size_t state_bytes;
+  int32_t n_groups;      /* 1 .. n                                                             */
+  int32_t max_rows;      /* at least the largest count of tokens (rows) of a group             */
+} pi_kv_shared_args;
+
 typedef struct pi_kv pi_kv;
 
 /* ABI version of this half of the library (PI_KV_ABI_VERSION). */
@@ -207,6 +221,26 @@ pi_status pi_kv_read(pi_kv* h, int32_t layer, const pi_kv_rows* k, const pi_kv_r
  * out 0 and lse -inf.
  */
 pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_batch* batch, void* stream);
+
+/*
+ * How much the sequences of each group share: plan[g] is the number of leading tokens of group g whose pages all
+ * of its sequences name alike and that all of them held before this batch's tokens, rounded down to whole blocks; 0 for a
+ * group of one.  plan[n_groups + i] is that of seqs[i]'s group.  It holds for every layer, and until lens or table
+ * change, for the same seqs, starts and groups.
+ */
+pi_status pi_kv_share(pi_kv* h, const pi_kv_batch* batch, const int32_t* groups, int32_t n_groups, int32_t* plan,
+                      void* stream);
+
+/* Bytes of scratch that pi_kv_attend_shared takes for `rows` rows.  Host only. */
+pi_status pi_kv_state_bytes(const pi_kv* h, int32_t rows, size_t* bytes);
+
+/*
+ * pi_kv_attend for groups: the same results up to the order of sums, but the first plan[g] tokens of a group are read
+ * once, from its first sequence's pages, for all rows of the group.  Whole sequences: window and sinks are 0.  A plan
+ * that was not made for these sequences gives rows that mean nothing (and touches no other memory).
+ */
+pi_status pi_kv_attend_shared(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_shared_args* shared,
+                              const pi_kv_batch* batch, void* stream);
 
 /*
  * Make room for counts[i] more tokens of seqs[i] and count them in lens: free pages are taken from the
