@@ -31,14 +31,20 @@ __device__ __forceinline__ f32x4 product(const typename ActT<ACT>::V8& x, const 
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, w, c, 0, 0, 0);
 }
 
+// The exponent that makes operands of codes, in a register: an instruction that masks and joins takes one constant.
+template <int ACT>
+__device__ __forceinline__ unsigned sixteen() {
+  unsigned one = Code<ACT>::kOne;
+  asm volatile("" : "+v"(one));
+  return one;
+}
+
 // One word: eight columns of a row as 24 + q.
 template <int ACT>
-__device__ __forceinline__ typename ActT<ACT>::V8 operand(unsigned w) {
-  using C = Code<ACT>;
+__device__ __forceinline__ typename ActT<ACT>::V8 operand(unsigned w, unsigned one) {
   u32x4 r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    r[j] = (__builtin_amdgcn_alignbit(w, w, 4 * j) & C::kMask) | C::kOne;
+  for (int j = 0; j < 4; ++j) r[j] = (__builtin_amdgcn_alignbit(w, w, 4 * j) & Code<ACT>::kMask) | one;
   return __builtin_bit_cast(typename ActT<ACT>::V8, r);
 }
 
@@ -82,9 +88,7 @@ __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__
   *reinterpret_cast<unsigned*>(to + 2048 + lane * 4) = s;
 }
 
-// ---- the product ---------------------------------------------------------------------------------------
-
-constexpr int kLinearWaves = 8;
+// ---- one to 64 rows ------------------------------------------------------------------------------------
 
 // A slab of one tile as a wave holds it.
 struct Slab {
@@ -99,84 +103,53 @@ __device__ __forceinline__ Slab load_slab(const uint8_t* p) {
   s.scale = ld_stream(reinterpret_cast<const u32x4*>(p + 2048) + lane % 16);
   return s;
 }
+__device__ __forceinline__ float scale_of(const Slab& s, int k) { return (float)as_h2(s.scale[k / 2])[k % 2]; }
 
-// A workgroup takes T tiles of 16 outputs and NB tiles of 16 rows; its waves take the slabs in turn.  Row t of a tile
-// of rows stands in row 4 (t % 4) + t / 4 of the product, so that up to four rows leave one sum a lane (NI of 4
-// registers hold rows).
-template <int ACT, int NB, int NI, int T>
-__global__ __launch_bounds__(WAVE* kLinearWaves) void k_linear(const LinearArgs A) {
-  using E = typename ActT<ACT>::T;
-  using V8 = typename ActT<ACT>::V8;
-  extern __shared__ float s_part[];   // [waves][T][NB][NI][64]
-  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  const int waves = blockDim.x / WAVE;
-  const int groups = (A.tiles + T - 1) / T;
-  const int tile0 = (int)(blockIdx.x % groups) * T, row0 = (int)(blockIdx.x / groups) * (16 * NB);
-  const int g = lane >> 4, slot = lane & 15;
-  const E* xrow[NB];
-  bool live[NB];
+template <int ACT>
+__device__ __forceinline__ typename ActT<ACT>::V8 minus24() {
+  constexpr unsigned m = Code<ACT>::kMinus;
+  return __builtin_bit_cast(typename ActT<ACT>::V8, u32x4{m, m, m, m});
+}
+
+// Products of NB tiles that are still to be scaled and added: this is done beside the next ones, so that neither the
+// matrix instructions nor the vector ALU wait for each other's results.
+template <int NB> struct Late {
+  f32x4 p[NB];
+  float scale = 0.0f;
+  __device__ __forceinline__ Late() {
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int t = row0 + 16 * b + (slot >> 2) + 4 * (slot & 3);
-    live[b] = t < A.rows;
-    xrow[b] = static_cast<const E*>(A.x) + (int64_t)(live[b] ? t : 0) * A.x_stride;
+    for (int b = 0; b < NB; ++b) p[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  const uint8_t* from[T];
+  __device__ __forceinline__ void set(const f32x4 (&now)[NB], float s) {
 #pragma unroll
-  for (int j = 0; j < T; ++j) from[j] = A.packed + (size_t)min(tile0 + j, A.tiles - 1) * A.slabs * kSlabBytes;
-
-  float acc[T][NB][NI];
-#pragma unroll
-  for (int j = 0; j < T; ++j)
+    for (int b = 0; b < NB; ++b) p[b] = now[b];
+    scale = s;
+  }
+  __device__ __forceinline__ void add(float (&acc)[NB][4]) const {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) acc[j][b][i] = 0.0f;
-  const V8 minus = __builtin_bit_cast(V8, u32x4{Code<ACT>::kMinus, Code<ACT>::kMinus, Code<ACT>::kMinus, Code<ACT>::kMinus});
-
-  Slab next[T];
-  if (wave < A.slabs) {
-#pragma unroll
-    for (int j = 0; j < T; ++j) next[j] = load_slab(from[j] + (size_t)wave * kSlabBytes);
+      for (int i = 0; i < 4; ++i) acc[b][i] = fmaf(p[b][i], scale, acc[b][i]);
   }
-  for (int s = wave; s < A.slabs; s += waves) {
-    Slab cur[T];
+};
+// One matrix instruction, then what the vector ALU does meanwhile.
+template <int N>
+__device__ __forceinline__ void interleave() {
 #pragma unroll
-    for (int j = 0; j < T; ++j) cur[j] = next[j];
-    const int col = s * kSlabCols + 8 * g;
-    if (s + waves < A.slabs) {
-#pragma unroll
-      for (int j = 0; j < T; ++j) next[j] = load_slab(from[j] + (size_t)(s + waves) * kSlabBytes);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // columns past the end have q = 0 and scale 0, whatever x they meet: the row's own last
-      const int at = min(col + 32 * k, A.d_in - 8);
-      V8 x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        x[b] = V8{};
-        if (live[b]) x[b] = *reinterpret_cast<const V8*>(xrow[b] + at);
-      }
-      f32x4 c[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) c[b] = product<ACT>(x[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-      for (int j = 0; j < T; ++j) {
-        const V8 w = operand<ACT>(cur[j].code[k / 4][k % 4]);
-        const float scale = (float)as_h2(cur[j].scale[k / 2])[k % 2];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const f32x4 p = product<ACT>(x[b], w, c[b]);
-#pragma unroll
-          for (int i = 0; i < NI; ++i) acc[j][b][i] = fmaf(p[i], scale, acc[j][b][i]);
-        }
-      }
-    }
+  for (int b = 0; b < N; ++b) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
   }
+}
 
-  // ---- the waves' sums, in their order, and out ----------------------------------------------------------
+// The waves' sums [tile][rows' tile][i][lane], joined in the waves' order, and out.  Sum i of lane group q is row
+// 4 q + i of its tile; with one sum a lane, row q.
+template <int ACT, int NB, int NI, int T>
+__device__ __forceinline__ void join_waves(const LinearArgs& A, float* s_part, const float (&acc)[T][NB][NI], int tile0,
+                                           int row0, int wave, int waves) {
+  using E = typename ActT<ACT>::T;
   constexpr int kSums = T * NB * NI * WAVE;
+  const int lane = threadIdx.x & (WAVE - 1);
 #pragma unroll
   for (int j = 0; j < T; ++j)
 #pragma unroll
@@ -185,32 +158,336 @@ __global__ __launch_bounds__(WAVE* kLinearWaves) void k_linear(const LinearArgs 
       for (int i = 0; i < NI; ++i) s_part[wave * kSums + ((j * NB + b) * NI + i) * WAVE + lane] = acc[j][b][i];
   __syncthreads();
   for (int k = threadIdx.x; k < kSums; k += blockDim.x) {
-    const int n16 = k % 16, q = k / 16 % 4, j = k / (WAVE * NI * NB), b = k / (WAVE * NI) % NB, i = k / WAVE % NI;
-    const int t = row0 + 16 * b + q + 4 * i, n = (tile0 + j) * 16 + n16;
+    // neighbouring threads have neighbouring outputs of a row
+    const int n = (tile0 * 16) + k % (16 * T), r = k / (16 * T), i = r % NI, q = r / NI % 4, b = r / (4 * NI);
+    const int t = row0 + 16 * b + NI * q + i;
     if (t >= A.rows || n >= A.d_out) continue;
-    float v = s_part[k];
-    for (int w = 1; w < waves; ++w) v += s_part[w * kSums + k];
+    const int at = (((k % (16 * T) / 16) * NB + b) * NI + i) * WAVE + 16 * q + k % 16;
+    float v = s_part[at];
+    for (int w = 1; w < waves; ++w) v += s_part[w * kSums + at];
     if (A.bias != nullptr) v += A.bias[n];
     if (A.add != nullptr) v += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
     static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)v;
   }
 }
 
-template <int ACT, int NB, int NI, int T>
-hipError_t linear_go(const LinearArgs& a, hipStream_t s) {
-  const long long grid = (long long)((a.tiles + T - 1) / T) * ((a.rows + 16 * NB - 1) / (16 * NB));
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  const int waves = a.slabs < kLinearWaves ? a.slabs : kLinearWaves;
-  hipLaunchKernelGGL((k_linear<ACT, NB, NI, T>), dim3((unsigned)grid), dim3(WAVE * waves),
-                     (size_t)waves * T * NB * NI * WAVE * sizeof(float), s, a);
+// Up to four rows: bound by reading the codes.  A workgroup takes one tile, its waves the slabs in turn, two of them
+// on their way while one is computed.  x goes through LDS, each wave's own slab of it, since as an operand each lane of
+// 64 would load a row's 16 bytes again for all of a tile's 16 slots.
+constexpr int kFewWaves = 8, kFewRows = 4;
+template <int ACT, int B>
+__global__ __launch_bounds__(WAVE* kFewWaves) void k_linear_few(const LinearArgs A) {
+  using E = typename ActT<ACT>::T;
+  using V8 = typename ActT<ACT>::V8;
+  __shared__ __align__(16) E s_x[kFewWaves][2][B][kSlabCols];
+  __shared__ float s_part[kFewWaves * WAVE];
+  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int waves = blockDim.x / WAVE, tile = blockIdx.x, g = lane >> 4;
+  const uint8_t* from = A.packed + (size_t)tile * A.slabs * kSlabBytes;
+  // this lane's four columns of a slab of each row; past the end the row's last: q and scale are 0 there
+  typedef E E4 __attribute__((ext_vector_type(4)));
+  E4 x[2][B];
+  auto fetch = [&](int s, E4 (&to)[B]) {
+    const int col = min(s * kSlabCols + 4 * lane, A.d_in - 4);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      to[b] = *reinterpret_cast<const E4*>(static_cast<const E*>(A.x) + (int64_t)min(b, A.rows - 1) * A.x_stride + col);
+  };
+  Slab w[2];
+  fetch(wave, x[0]);
+  w[0] = load_slab(from + (size_t)wave * kSlabBytes);
+  if (wave + waves < A.slabs) {
+    fetch(wave + waves, x[1]);
+    w[1] = load_slab(from + (size_t)(wave + waves) * kSlabBytes);
+  }
+  float acc = 0.0f;
+  const V8 minus = minus24<ACT>();
+  const unsigned one = sixteen<ACT>();
+  const int row = min((lane & 15) >> 2, B - 1);
+  auto step = [&](int s, int buf) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) *reinterpret_cast<E4*>(&s_x[wave][buf][b][4 * lane]) = x[buf][b];
+    const Slab cur = w[buf];
+    if (s + 2 * waves < A.slabs) {
+      fetch(s + 2 * waves, x[buf]);
+      w[buf] = load_slab(from + (size_t)(s + 2 * waves) * kSlabBytes);
+    }
+    __builtin_amdgcn_wave_barrier();   // a wave's LDS operations are done in their order
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const V8 v = *reinterpret_cast<const V8*>(&s_x[wave][buf][row][32 * k + 8 * g]);
+      const f32x4 c = product<ACT>(v, minus, f32x4{0.f, 0.f, 0.f, 0.f});
+      const f32x4 p = product<ACT>(v, operand<ACT>(cur.code[k / 4][k % 4], one), c);
+      acc = fmaf(p[0], scale_of(cur, k), acc);
+    }
+    __builtin_amdgcn_wave_barrier();
+  };
+  for (int s = wave; s < A.slabs; s += 2 * waves) {
+    step(s, 0);
+    if (s + waves < A.slabs) step(s + waves, 1);
+  }
+  const float sums[1][1][1] = {{{acc}}};
+  join_waves<ACT, 1, 1, 1>(A, s_part, sums, tile, 0, wave, waves);
+}
+
+// x on its way to LDS: no registers, and in the order in which it lies in memory, 128 bytes of a row by eight lanes
+// (as operands, lane after lane another row, an L1 takes 64 cycles for a load instead of 16).  A tile of 16 rows and 64
+// columns is [16][8] units of 16 bytes; unit u of row r holds columns 8 (u ^ r % 8) .., which keeps the lanes of an
+// operand on banks of their own.
+constexpr int kStage = 64;                                   // columns
+template <class V8> using XTile = V8[16][kStage / 8];
+template <class E, class V8>
+__device__ __forceinline__ void bring_rows(const E* row, int col, int end, V8* to) {   // 8 rows: lane l's is l / 8
+  const int lane = threadIdx.x & (WAVE - 1), at = min(col + 8 * ((lane ^ (lane >> 3)) & 7), end - 8);
+  __builtin_amdgcn_global_load_lds(
+      reinterpret_cast<const __attribute__((address_space(1))) unsigned*>(reinterpret_cast<uintptr_t>(row + at)),
+      (__attribute__((address_space(3))) unsigned*)to, 16, 0, 0);
+}
+// Operand of group k (0 or 1) of a tile.
+template <class V8>
+__device__ __forceinline__ V8 x_operand(const V8 (&x)[16][kStage / 8], int k) {
+  const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
+  return x[r][(4 * k + (lane >> 4)) ^ (r & 7)];
+}
+// At most N of this wave's loads are still on their way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Up to 16 NB rows; T tiles a workgroup, whose waves take the slabs in turn.  Each wave brings the x of its own slabs to
+// LDS, DEPTH - 1 stages of 64 columns ahead; codes come a slab ahead.
+template <int ACT, int NB, int T, int W, int DEPTH>
+__global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) {
+  using E = typename ActT<ACT>::T;
+  using V8 = typename ActT<ACT>::V8;
+  constexpr int kX = W * DEPTH * NB * 16 * kStage * 2, kPart = W * T * NB * 4 * WAVE * 4;
+  __shared__ __align__(16) char s_mem[kX > kPart ? kX : kPart];
+  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int waves = blockDim.x / WAVE, tile0 = (int)blockIdx.x * T;
+  XTile<V8>(*s_x)[NB] = reinterpret_cast<XTile<V8>(*)[NB]>(s_mem) + wave * DEPTH;
+  const E* xrow[2 * NB];
+#pragma unroll
+  for (int e = 0; e < 2 * NB; ++e)   // rows past the end are not stored
+    xrow[e] = static_cast<const E*>(A.x) + (int64_t)min(8 * e + (lane >> 3), A.rows - 1) * A.x_stride;
+  const uint8_t* from[T];
+#pragma unroll
+  for (int j = 0; j < T; ++j) from[j] = A.packed + (size_t)min(tile0 + j, A.tiles - 1) * A.slabs * kSlabBytes;
+
+  float acc[T][NB][4];
+#pragma unroll
+  for (int j = 0; j < T; ++j)
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][b][i] = 0.0f;
+  const V8 minus = minus24<ACT>();
+  const unsigned one = sixteen<ACT>();
+  // stage i of this wave: columns of slab wave + i / 4 waves; past its last the last slab again, which nobody reads.
+  // Columns past the end have q = 0 and scale 0, whatever x they meet: the row's own last.
+  auto slab_of = [&](int i) { return min(wave + i / 4 * waves, A.slabs - 1); };
+  auto bring = [&](int i) {
+    const int col = slab_of(i) * kSlabCols + i % 4 * kStage;
+#pragma unroll
+    for (int e = 0; e < 2 * NB; ++e) bring_rows(xrow[e], col, A.d_in, &s_x[i % DEPTH][e / 2][8 * (e % 2)][0]);
+  };
+  Late<NB> late;
+  Slab w[2][T];   // the slab at hand and the next one
+#pragma unroll
+  for (int j = 0; j < T; ++j) w[0][j] = load_slab(from[j] + (size_t)wave * kSlabBytes);
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) bring(i);
+  auto step = [&](int s, int i0, const Slab (&cur)[T], Slab (&next)[T]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      // the stage's x: behind it are the DEPTH - 2 stages after it, and the next slab's codes where they began since
+      constexpr int kAfter = (DEPTH - 2) * 2 * NB;
+      if (q > 0 && q < DEPTH)
+        wait_loads<kAfter + 3 * T>();
+      else
+        wait_loads<kAfter>();
+      if (q == 0) {   // this slab's codes are there too: the compiler shall wait for them here, before the next loads
+#pragma unroll
+        for (int j = 0; j < T; ++j) asm volatile("" ::"v"(cur[j].code[0]), "v"(cur[j].code[1]), "v"(cur[j].scale));
+      }
+      bring(i0 + q + DEPTH - 1);
+      if (q == 0) {
+#pragma unroll
+        for (int j = 0; j < T; ++j) next[j] = load_slab(from[j] + (size_t)min(s + waves, A.slabs - 1) * kSlabBytes);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        V8 v[NB];
+        f32x4 c[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          v[b] = x_operand(s_x[(i0 + q) % DEPTH][b], k);
+          c[b] = product<ACT>(v[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
+        }
+#pragma unroll
+        for (int j = 0; j < T; ++j) {
+          const V8 u = operand<ACT>(cur[j].code[q / 2][2 * (q % 2) + k], one);
+          f32x4 now[NB];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) now[b] = product<ACT>(v[b], u, c[b]);
+          late.add(acc[(j + T - 1) % T]);
+          late.set(now, scale_of(cur[j], 2 * q + k));
+          interleave<NB>();
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int i0 = 0;
+  for (int s = wave; s < A.slabs; s += 2 * waves, i0 += 8) {
+    step(s, i0, w[0], w[1]);
+    if (s + waves >= A.slabs) break;
+    step(s + waves, i0 + 4, w[1], w[0]);
+  }
+  late.add(acc[T - 1]);
+  wait_loads<0>();      // nothing is on its way to LDS any more
+  __syncthreads();
+  join_waves<ACT, NB, 4, T>(A, reinterpret_cast<float*>(s_mem), acc, tile0, 0, wave, waves);
+}
+
+// ---- more than 64 rows ---------------------------------------------------------------------------------
+
+// Bound by the vector ALU (an fp32 multiply-add for each output and group, as long as the product itself) and the matrix
+// instructions.  A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x goes to LDS without passing
+// registers, in the operands' order, 64 columns while the 64 before are used; codes come straight to registers.
+constexpr int kTileM = 128, kTileN = 128;
+template <int ACT>
+__global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
+  using E = typename ActT<ACT>::T;
+  using V8 = typename ActT<ACT>::V8;
+  __shared__ XTile<V8> s_x[2][kTileM / 16];
+  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int g = lane >> 4, wm = wave >> 1, wn = wave & 1;
+  const int across = (A.tiles + kTileN / 16 - 1) / (kTileN / 16);
+  const int row0 = (int)(blockIdx.x / across) * kTileM, tile0 = (int)(blockIdx.x % across) * (kTileN / 16) + 4 * wn;
+  const E* xrow[4];   // this wave brings rows 32 wave .. of a stage
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    xrow[e] = static_cast<const E*>(A.x) + (int64_t)min(row0 + 32 * wave + 8 * e + (lane >> 3), A.rows - 1) * A.x_stride;
+  const uint8_t* from[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) from[j] = A.packed + (size_t)min(tile0 + j, A.tiles - 1) * A.slabs * kSlabBytes;
+  auto bring = [&](int stage, int buf) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      bring_rows(xrow[e], stage * kStage, A.d_in, &s_x[buf][2 * wave + e / 2][8 * (e % 2)][0]);
+  };
+  float acc[4][4][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][b][i] = 0.0f;
+  const V8 minus = minus24<ACT>();
+  const unsigned one = sixteen<ACT>();
+  const int stages = A.slabs * (kSlabCols / kStage);
+
+  Late<4> late;
+  u32x4 code[4], ncode[4], scale[4], nscale[4];
+  auto codes = [&](int piece, u32x4 (&to)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      to[j] = *(reinterpret_cast<const u32x4*>(from[j] + (size_t)(piece / 2) * kSlabBytes + 1024 * (piece % 2)) + lane);
+  };
+  auto scales = [&](int slab, u32x4 (&to)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      to[j] = *(reinterpret_cast<const u32x4*>(from[j] + (size_t)slab * kSlabBytes + 2048) + (lane & 15));
+  };
+  bring(0, 0);
+  codes(0, ncode);
+  scales(0, nscale);
+  for (int slab = 0; slab < A.slabs; ++slab) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) scale[j] = nscale[j];
+#pragma unroll
+    for (int q = 0; q < kSlabCols / kStage; ++q) {
+      const int stage = slab * (kSlabCols / kStage) + q;
+      wait_loads<0>();   // this wave's part of the stage, and its codes
+      __syncthreads();
+      if (q % 2 == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) code[j] = ncode[j];
+      }
+      bring(min(stage + 1, stages - 1), (q + 1) & 1);   // after the last stage nobody reads it
+      if (q % 2 == 0) codes(min(2 * slab + q / 2 + 1, 2 * A.slabs - 1), ncode);
+      if (q == 2) scales(min(slab + 1, A.slabs - 1), nscale);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        V8 v[4];
+        f32x4 c[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          v[b] = x_operand(s_x[q & 1][4 * wm + b], k);
+          c[b] = product<ACT>(v[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const V8 w = operand<ACT>(code[j][2 * (q % 2) + k], one);
+          const int group = 2 * q + k;
+          f32x4 now[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) now[b] = product<ACT>(v[b], w, c[b]);
+          late.add(acc[(j + 3) % 4]);
+          late.set(now, (float)as_h2(scale[j][group / 2])[group % 2]);
+          interleave<4>();
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  late.add(acc[3]);
+  wait_loads<0>();   // nothing is on its way to LDS when the workgroup ends
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = (tile0 + j) * 16 + (lane & 15);
+    if (n >= A.d_out) continue;
+    const float bias = A.bias != nullptr ? A.bias[n] : 0.0f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = row0 + 64 * wm + 16 * b + 4 * g + i;
+        if (t >= A.rows) continue;
+        float y = acc[j][b][i] + bias;
+        if (A.add != nullptr) y += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
+        static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)y;
+      }
+  }
+}
+
+template <int ACT, int B>
+hipError_t few_go(const LinearArgs& a, hipStream_t s) {
+  const int waves = a.slabs < kFewWaves ? a.slabs : kFewWaves;
+  hipLaunchKernelGGL((k_linear_few<ACT, B>), dim3((unsigned)a.tiles), dim3(WAVE * waves), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int ACT, int NB, int T, int W, int DEPTH>
+hipError_t rows_go(const LinearArgs& a, hipStream_t s) {
+  const int waves = a.slabs < W ? a.slabs : W;
+  hipLaunchKernelGGL((k_linear_rows<ACT, NB, T, W, DEPTH>), dim3((unsigned)((a.tiles + T - 1) / T)), dim3(WAVE * waves), 0, s, a);
   return hipGetLastError();
 }
 
 template <int ACT>
 hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
-  if (a.rows <= 4) return linear_go<ACT, 1, 1, 1>(a, s);
-  if (a.rows <= 16) return linear_go<ACT, 1, 4, 2>(a, s);
-  return linear_go<ACT, 2, 4, 2>(a, s);
+  if (a.rows == 1) return few_go<ACT, 1>(a, s);
+  if (a.rows <= kFewRows) return few_go<ACT, kFewRows>(a, s);
+  if (a.rows <= 16) return rows_go<ACT, 1, 2, 8, 4>(a, s);
+  if (a.rows <= 32) return rows_go<ACT, 2, 2, 8, 2>(a, s);
+  if (a.rows <= 64) return rows_go<ACT, 4, 2, 4, 2>(a, s);
+  const long long grid = (long long)((a.tiles + kTileN / 16 - 1) / (kTileN / 16)) * ((a.rows + kTileM - 1) / kTileM);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_linear_tile<ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace
