@@ -123,6 +123,7 @@ template <int NB> struct Late {
   __device__ __forceinline__ void set(const f32x4 (&now)[NB], float s) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) p[b] = now[b];
+    asm volatile("" : "+v"(s));
     scale = s;
   }
   __device__ __forceinline__ void add(float (&acc)[NB][4]) const {
@@ -176,56 +177,60 @@ __device__ __forceinline__ void join_waves(const LinearArgs& A, float* s_part, c
 // 64 would load a row's 16 bytes again for all of a tile's 16 slots.
 constexpr int kFewWaves = 8, kFewRows = 4;
 template <int ACT, int B>
-__global__ __launch_bounds__(WAVE* kFewWaves) void k_linear_few(const LinearArgs A) {
+__global__ __launch_bounds__(WAVE* kFewWaves, 5) void k_linear_few(const LinearArgs A) {
   using E = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
+  typedef E E4 __attribute__((ext_vector_type(4)));
   __shared__ __align__(16) E s_x[kFewWaves][2][B][kSlabCols];
   __shared__ float s_part[kFewWaves * WAVE];
   const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int waves = blockDim.x / WAVE, tile = blockIdx.x, g = lane >> 4;
   const uint8_t* from = A.packed + (size_t)tile * A.slabs * kSlabBytes;
-  // this lane's four columns of a slab of each row; past the end the row's last: q and scale are 0 there
-  typedef E E4 __attribute__((ext_vector_type(4)));
-  E4 x[2][B];
-  auto fetch = [&](int s, E4 (&to)[B]) {
+  const E* xrow[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) xrow[b] = static_cast<const E*>(A.x) + (int64_t)min(b, A.rows - 1) * A.x_stride;
+  // this lane's four columns of a slab of each row, and the codes; past the last slab the last again, which nobody uses.
+  // Columns past the end have q = 0 and scale 0, whatever x they meet: the row's own last.
+  struct Stage {
+    E4 x[B];
+    Slab w;
+  };
+  auto load = [&](int s, Stage& to) {
+    s = min(s, A.slabs - 1);
     const int col = min(s * kSlabCols + 4 * lane, A.d_in - 4);
 #pragma unroll
-    for (int b = 0; b < B; ++b)
-      to[b] = *reinterpret_cast<const E4*>(static_cast<const E*>(A.x) + (int64_t)min(b, A.rows - 1) * A.x_stride + col);
+    for (int b = 0; b < B; ++b) to.x[b] = *reinterpret_cast<const E4*>(xrow[b] + col);
+    to.w = load_slab(from + (size_t)s * kSlabBytes);
   };
-  Slab w[2];
-  fetch(wave, x[0]);
-  w[0] = load_slab(from + (size_t)wave * kSlabBytes);
-  if (wave + waves < A.slabs) {
-    fetch(wave + waves, x[1]);
-    w[1] = load_slab(from + (size_t)(wave + waves) * kSlabBytes);
-  }
   float acc = 0.0f;
   const V8 minus = minus24<ACT>();
   const unsigned one = sixteen<ACT>();
   const int row = min((lane & 15) >> 2, B - 1);
-  auto step = [&](int s, int buf) {
+  auto step = [&](int s, const Stage& cur, Stage& later, int buf) {
+    load(s + 2 * waves, later);
 #pragma unroll
-    for (int b = 0; b < B; ++b) *reinterpret_cast<E4*>(&s_x[wave][buf][b][4 * lane]) = x[buf][b];
-    const Slab cur = w[buf];
-    if (s + 2 * waves < A.slabs) {
-      fetch(s + 2 * waves, x[buf]);
-      w[buf] = load_slab(from + (size_t)(s + 2 * waves) * kSlabBytes);
-    }
+    for (int b = 0; b < B; ++b) *reinterpret_cast<E4*>(&s_x[wave][buf][b][4 * lane]) = cur.x[b];
     __builtin_amdgcn_wave_barrier();   // a wave's LDS operations are done in their order
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const V8 v = *reinterpret_cast<const V8*>(&s_x[wave][buf][row][32 * k + 8 * g]);
       const f32x4 c = product<ACT>(v, minus, f32x4{0.f, 0.f, 0.f, 0.f});
-      const f32x4 p = product<ACT>(v, operand<ACT>(cur.code[k / 4][k % 4], one), c);
-      acc = fmaf(p[0], scale_of(cur, k), acc);
+      const f32x4 p = product<ACT>(v, operand<ACT>(cur.w.code[k / 4][k % 4], one), c);
+      acc = fmaf(p[0], scale_of(cur.w, k), acc);
     }
     __builtin_amdgcn_wave_barrier();
   };
-  for (int s = wave; s < A.slabs; s += 2 * waves) {
-    step(s, 0);
-    if (s + waves < A.slabs) step(s + waves, 1);
+  Stage st[3];
+  load(wave, st[0]);
+  load(wave + waves, st[1]);
+  for (int s = wave;; s += 6 * waves) {
+#pragma unroll
+    for (int e = 0; e < 6; ++e) {
+      step(s + e * waves, st[e % 3], st[(e + 2) % 3], e % 2);
+      if (s + (e + 1) * waves >= A.slabs) goto out;
+    }
   }
+out:
   const float sums[1][1][1] = {{{acc}}};
   join_waves<ACT, 1, 1, 1>(A, s_part, sums, tile, 0, wave, waves);
 }
@@ -236,12 +241,17 @@ __global__ __launch_bounds__(WAVE* kFewWaves) void k_linear_few(const LinearArgs
 // operand on banks of their own.
 constexpr int kStage = 64;                                   // columns
 template <class V8> using XTile = V8[16][kStage / 8];
-template <class E, class V8>
-__device__ __forceinline__ void bring_rows(const E* row, int col, int end, V8* to) {   // 8 rows: lane l's is l / 8
-  const int lane = threadIdx.x & (WAVE - 1), at = min(col + 8 * ((lane ^ (lane >> 3)) & 7), end - 8);
-  __builtin_amdgcn_global_load_lds(
-      reinterpret_cast<const __attribute__((address_space(1))) unsigned*>(reinterpret_cast<uintptr_t>(row + at)),
-      (__attribute__((address_space(3))) unsigned*)to, 16, 0, 0);
+// Where lane l's part of a row of a stage begins, in bytes of the row: unit l % 8 of row l / 8 (of eight).  Columns past the
+// end have q = 0 and scale 0, whatever x they meet: the row's own last.
+__device__ __forceinline__ unsigned stage_byte(int col, int end) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  return 2u * (unsigned)min(col + 8 * ((lane ^ (lane >> 3)) & 7), end - 8);
+}
+// 16 bytes a lane from base + at to LDS, lane after lane.
+__device__ __forceinline__ void bring(const void* base, unsigned at, void* to) {
+  const auto* from = reinterpret_cast<const __attribute__((address_space(1))) char*>(reinterpret_cast<uintptr_t>(base));
+  __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) unsigned*>(from + at),
+                                   (__attribute__((address_space(3))) unsigned*)to, 16, 0, 0);
 }
 // Operand of group k (0 or 1) of a tile.
 template <class V8>
@@ -252,12 +262,13 @@ __device__ __forceinline__ V8 x_operand(const V8 (&x)[16][kStage / 8], int k) {
 // At most N of this wave's loads are still on their way.
 template <int N>
 __device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0f70);
+  asm volatile("" ::: "memory");
 }
 
 // Up to 16 NB rows; T tiles a workgroup, whose waves take the slabs in turn.  Each wave brings the x of its own slabs to
-// LDS, DEPTH - 1 stages of 64 columns ahead; codes come a slab ahead.
-template <int ACT, int NB, int T, int W, int DEPTH>
+// LDS, DEPTH - 1 stages of 64 columns ahead; codes come PRE slabs ahead.
+template <int ACT, int NB, int T, int W, int DEPTH, int PRE>
 __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) {
   using E = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
@@ -266,10 +277,10 @@ __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) 
   const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int waves = blockDim.x / WAVE, tile0 = (int)blockIdx.x * T;
   XTile<V8>(*s_x)[NB] = reinterpret_cast<XTile<V8>(*)[NB]>(s_mem) + wave * DEPTH;
-  const E* xrow[2 * NB];
+  unsigned xrow[2 * NB];
 #pragma unroll
   for (int e = 0; e < 2 * NB; ++e)   // rows past the end are not stored
-    xrow[e] = static_cast<const E*>(A.x) + (int64_t)min(8 * e + (lane >> 3), A.rows - 1) * A.x_stride;
+    xrow[e] = 2u * (unsigned)min(8 * e + (lane >> 3), A.rows - 1) * (unsigned)A.x_stride;
   const uint8_t* from[T];
 #pragma unroll
   for (int j = 0; j < T; ++j) from[j] = A.packed + (size_t)min(tile0 + j, A.tiles - 1) * A.slabs * kSlabBytes;
@@ -283,38 +294,31 @@ __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) 
       for (int i = 0; i < 4; ++i) acc[j][b][i] = 0.0f;
   const V8 minus = minus24<ACT>();
   const unsigned one = sixteen<ACT>();
-  // stage i of this wave: columns of slab wave + i / 4 waves; past its last the last slab again, which nobody reads.
-  // Columns past the end have q = 0 and scale 0, whatever x they meet: the row's own last.
-  auto slab_of = [&](int i) { return min(wave + i / 4 * waves, A.slabs - 1); };
-  auto bring = [&](int i) {
-    const int col = slab_of(i) * kSlabCols + i % 4 * kStage;
+  // past a wave's last slab the matrix's last again, which nobody uses
+  auto bring_stage = [&](int s, int q, int i) {   // stage q of slab s, the wave's i-th
+    const unsigned at = stage_byte(min(s, A.slabs - 1) * kSlabCols + q * kStage, A.d_in);
 #pragma unroll
-    for (int e = 0; e < 2 * NB; ++e) bring_rows(xrow[e], col, A.d_in, &s_x[i % DEPTH][e / 2][8 * (e % 2)][0]);
+    for (int e = 0; e < 2 * NB; ++e) bring(A.x, xrow[e] + at, &s_x[i % DEPTH][e / 2][8 * (e % 2)][0]);
+  };
+  auto load = [&](int s, Slab (&to)[T]) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) to[j] = load_slab(from[j] + (size_t)min(s, A.slabs - 1) * kSlabBytes);
   };
   Late<NB> late;
-  Slab w[2][T];   // the slab at hand and the next one
-#pragma unroll
-  for (int j = 0; j < T; ++j) w[0][j] = load_slab(from[j] + (size_t)wave * kSlabBytes);
-#pragma unroll
-  for (int i = 0; i < DEPTH - 1; ++i) bring(i);
-  auto step = [&](int s, int i0, const Slab (&cur)[T], Slab (&next)[T]) {
+  Slab w[PRE + 1][T];   // the slab at hand and the next ones
+  // A stage is complete when all that was asked for before it is: behind it are the DEPTH - 2 stages after it, and a
+  // slab's codes where they were asked for since.
+  auto step = [&](int s, const Slab (&cur)[T], Slab (&later)[T]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      // the stage's x: behind it are the DEPTH - 2 stages after it, and the next slab's codes where they began since
       constexpr int kAfter = (DEPTH - 2) * 2 * NB;
       if (q > 0 && q < DEPTH)
         wait_loads<kAfter + 3 * T>();
       else
         wait_loads<kAfter>();
-      if (q == 0) {   // this slab's codes are there too: the compiler shall wait for them here, before the next loads
-#pragma unroll
-        for (int j = 0; j < T; ++j) asm volatile("" ::"v"(cur[j].code[0]), "v"(cur[j].code[1]), "v"(cur[j].scale));
-      }
-      bring(i0 + q + DEPTH - 1);
-      if (q == 0) {
-#pragma unroll
-        for (int j = 0; j < T; ++j) next[j] = load_slab(from[j] + (size_t)min(s + waves, A.slabs - 1) * kSlabBytes);
-      }
+      bring_stage(s + (q + DEPTH - 1) / 4 * waves, (q + DEPTH - 1) % 4, q + DEPTH - 1);
+      __builtin_amdgcn_sched_barrier(0);   // the counts above go by this order
+      if (q == 0) load(s + PRE * waves, later);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) 
         f32x4 c[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          v[b] = x_operand(s_x[(i0 + q) % DEPTH][b], k);
+          v[b] = x_operand(s_x[q % DEPTH][b], k);
           c[b] = product<ACT>(v[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
         }
 #pragma unroll
@@ -339,12 +343,19 @@ __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) 
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  int i0 = 0;
-  for (int s = wave; s < A.slabs; s += 2 * waves, i0 += 8) {
-    step(s, i0, w[0], w[1]);
-    if (s + waves >= A.slabs) break;
-    step(s + waves, i0 + 4, w[1], w[0]);
+  static_assert(DEPTH == 2 || DEPTH == 4, "a slab's stages fill the ring a whole number of times");
+#pragma unroll
+  for (int e = 0; e < PRE; ++e) load(wave + e * waves, w[e]);
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) bring_stage(wave, i, i);
+  for (int s = wave;; s += (PRE + 1) * waves) {
+#pragma unroll
+    for (int e = 0; e <= PRE; ++e) {
+      step(s + e * waves, w[e], w[(e + PRE) % (PRE + 1)]);
+      if (s + (e + 1) * waves >= A.slabs) goto out;
+    }
   }
+out:
   late.add(acc[T - 1]);
   wait_loads<0>();      // nothing is on its way to LDS any more
   __syncthreads();
@@ -354,29 +365,48 @@ __global__ __launch_bounds__(WAVE* W, 2) void k_linear_rows(const LinearArgs A) 
 // ---- more than 64 rows ---------------------------------------------------------------------------------
 
 // Bound by the vector ALU (an fp32 multiply-add for each output and group, as long as the product itself) and the matrix
-// instructions.  A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x goes to LDS without passing
-// registers, in the operands' order, 64 columns while the 64 before are used; codes come straight to registers.
+// instructions.  A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x, codes and scales go to LDS
+// without passing registers: x in stages of 64 columns, two ahead of the one in use, codes two stages ahead too.
 constexpr int kTileM = 128, kTileN = 128;
 template <int ACT>
 __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
   using E = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
-  __shared__ XTile<V8> s_x[2][kTileM / 16];
+  constexpr int kTiles = kTileN / 16, kRing = 3;
+  __shared__ __align__(16) char s_mem[kRing * kTileM * kStage * 2 + 2 * kTiles * 1024 + 2 * 4 * 1024];
+  XTile<V8>(*s_x)[kTileM / 16] = reinterpret_cast<XTile<V8>(*)[kTileM / 16]>(s_mem);
+  u32x4(*s_code)[kTiles][WAVE] = reinterpret_cast<u32x4(*)[kTiles][WAVE]>(s_mem + kRing * kTileM * kStage * 2);
+  u32x4(*s_scale)[4][WAVE] = reinterpret_cast<u32x4(*)[4][WAVE]>(s_mem + kRing * kTileM * kStage * 2 + 2 * kTiles * 1024);
   const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int g = lane >> 4, wm = wave >> 1, wn = wave & 1;
-  const int across = (A.tiles + kTileN / 16 - 1) / (kTileN / 16);
-  const int row0 = (int)(blockIdx.x / across) * kTileM, tile0 = (int)(blockIdx.x % across) * (kTileN / 16) + 4 * wn;
-  const E* xrow[4];   // this wave brings rows 32 wave .. of a stage
+  const int across = (A.tiles + kTiles - 1) / kTiles;
+  const int row0 = (int)(blockIdx.x / across) * kTileM, tile0 = (int)(blockIdx.x % across) * kTiles;
+  const E* x0 = static_cast<const E*>(A.x) + (int64_t)row0 * A.x_stride;
+  unsigned xrow[4];   // this wave brings rows 32 wave .. of a stage; rows past the end are not stored
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    xrow[e] = static_cast<const E*>(A.x) + (int64_t)min(row0 + 32 * wave + 8 * e + (lane >> 3), A.rows - 1) * A.x_stride;
-  const uint8_t* from[4];
+    xrow[e] = 2u * (unsigned)min(32 * wave + 8 * e + (lane >> 3), A.rows - 1 - row0) * (unsigned)A.x_stride;
+  const size_t tile_bytes = (size_t)A.slabs * kSlabBytes;
+  // and the codes of tiles 2 wave and 2 wave + 1
+  const uint8_t* from[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) from[j] = A.packed + (size_t)min(tile0 + j, A.tiles - 1) * A.slabs * kSlabBytes;
-  auto bring = [&](int stage, int buf) {
+  for (int e = 0; e < 2; ++e) from[e] = A.packed + (size_t)min(tile0 + 2 * wave + e, A.tiles - 1) * tile_bytes;
+  const int stages = A.slabs * (kSlabCols / kStage);
+  // past the end the last again, which nobody uses
+  auto bring_x = [&](int stage, int slot) {
+    const unsigned at = stage_byte(min(stage, stages - 1) * kStage, A.d_in);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      bring_rows(xrow[e], stage * kStage, A.d_in, &s_x[buf][2 * wave + e / 2][8 * (e % 2)][0]);
+    for (int e = 0; e < 4; ++e) bring(x0, xrow[e] + at, &s_x[slot][2 * wave + e / 2][8 * (e % 2)][0]);
+  };
+  auto bring_codes = [&](int piece, int slot) {   // of 128 columns
+    const int p = min(piece, 2 * A.slabs - 1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      bring(from[e] + (size_t)(p / 2) * kSlabBytes + 1024 * (p % 2), 16u * lane, &s_code[slot][2 * wave + e][0]);
+  };
+  auto bring_scales = [&](int slab, int slot) {   // rows lane % 16 of the two tiles, twice
+    const uint8_t* p = from[0] + (size_t)min(slab, A.slabs - 1) * kSlabBytes + 2048;
+    bring(p, 16u * (lane & 15) + (lane & 16 ? (unsigned)(from[1] - from[0]) : 0u), &s_scale[slot][wave][0]);
   };
   float acc[4][4][4];
 #pragma unroll
@@ -387,45 +417,44 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
       for (int i = 0; i < 4; ++i) acc[j][b][i] = 0.0f;
   const V8 minus = minus24<ACT>();
   const unsigned one = sixteen<ACT>();
-  const int stages = A.slabs * (kSlabCols / kStage);
-
   Late<4> late;
-  u32x4 code[4], ncode[4], scale[4], nscale[4];
-  auto codes = [&](int piece, u32x4 (&to)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      to[j] = *(reinterpret_cast<const u32x4*>(from[j] + (size_t)(piece / 2) * kSlabBytes + 1024 * (piece % 2)) + lane);
-  };
-  auto scales = [&](int slab, u32x4 (&to)[4]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      to[j] = *(reinterpret_cast<const u32x4*>(from[j] + (size_t)slab * kSlabBytes + 2048) + (lane & 15));
-  };
-  bring(0, 0);
-  codes(0, ncode);
-  scales(0, nscale);
+  u32x4 code[4], scale[4];
+  bring_x(0, 0);
+  bring_codes(0, 0);
+  bring_scales(0, 0);
+  bring_x(1, 1);
+  int slot = 0;   // stage % kRing
   for (int slab = 0; slab < A.slabs; ++slab) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) scale[j] = nscale[j];
 #pragma unroll
     for (int q = 0; q < kSlabCols / kStage; ++q) {
       const int stage = slab * (kSlabCols / kStage) + q;
-      wait_loads<0>();   // this wave's part of the stage, and its codes
-      __syncthreads();
+      // what was asked for two stages ago is there; behind it is what the last stage asked for
+      if (q == 1) wait_loads<6>();
+      else if (q == 3) wait_loads<7>();
+      else wait_loads<4>();
+      // (not __syncthreads(), which waits for all that is on its way; every operand read so far has been used)
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      const int ahead = slot >= 1 ? slot - 1 : kRing - 1;
+      bring_x(stage + 2, ahead);
+      if (q % 2 == 0) bring_codes(2 * slab + q / 2 + 1, (q / 2 + 1) % 2);
+      if (q == 2) bring_scales(slab + 1, (slab + 1) & 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if (q == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) scale[j] = s_scale[slab & 1][2 * wn + j / 2][16 * (j % 2) + (lane & 15)];
+      }
       if (q % 2 == 0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) code[j] = ncode[j];
+        for (int j = 0; j < 4; ++j) code[j] = s_code[q / 2][4 * wn + j][lane];
       }
-      bring(min(stage + 1, stages - 1), (q + 1) & 1);   // after the last stage nobody reads it
-      if (q % 2 == 0) codes(min(2 * slab + q / 2 + 1, 2 * A.slabs - 1), ncode);
-      if (q == 2) scales(min(slab + 1, A.slabs - 1), nscale);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         V8 v[4];
         f32x4 c[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          v[b] = x_operand(s_x[q & 1][4 * wm + b], k);
+          v[b] = x_operand(s_x[slot][4 * wm + b], k);
           c[b] = product<ACT>(v[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
         }
 #pragma unroll
@@ -441,13 +470,14 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+      slot = slot == kRing - 1 ? 0 : slot + 1;
     }
   }
   late.add(acc[3]);
   wait_loads<0>();   // nothing is on its way to LDS when the workgroup ends
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int n = (tile0 + j) * 16 + (lane & 15);
+    const int n = (tile0 + 4 * wn + j) * 16 + (lane & 15);
     if (n >= A.d_out) continue;
     const float bias = A.bias != nullptr ? A.bias[n] : 0.0f;
 #pragma unroll
@@ -465,15 +495,16 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
 
 template <int ACT, int B>
 hipError_t few_go(const LinearArgs& a, hipStream_t s) {
-  const int waves = a.slabs < kFewWaves ? a.slabs : kFewWaves;
+  const int most = a.tiles <= 512 ? kFewWaves : kFewWaves / 2, waves = a.slabs < most ? a.slabs : most;
   hipLaunchKernelGGL((k_linear_few<ACT, B>), dim3((unsigned)a.tiles), dim3(WAVE * waves), 0, s, a);
   return hipGetLastError();
 }
 
-template <int ACT, int NB, int T, int W, int DEPTH>
+template <int ACT, int NB, int T, int W, int DEPTH, int PRE>
 hipError_t rows_go(const LinearArgs& a, hipStream_t s) {
   const int waves = a.slabs < W ? a.slabs : W;
-  hipLaunchKernelGGL((k_linear_rows<ACT, NB, T, W, DEPTH>), dim3((unsigned)((a.tiles + T - 1) / T)), dim3(WAVE * waves), 0, s, a);
+  hipLaunchKernelGGL((k_linear_rows<ACT, NB, T, W, DEPTH, PRE>), dim3((unsigned)((a.tiles + T - 1) / T)), dim3(WAVE * waves), 0,
+                     s, a);
   return hipGetLastError();
 }
 
@@ -481,9 +512,9 @@ template <int ACT>
 hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
   if (a.rows == 1) return few_go<ACT, 1>(a, s);
   if (a.rows <= kFewRows) return few_go<ACT, kFewRows>(a, s);
-  if (a.rows <= 16) return rows_go<ACT, 1, 2, 8, 4>(a, s);
-  if (a.rows <= 32) return rows_go<ACT, 2, 2, 8, 2>(a, s);
-  if (a.rows <= 64) return rows_go<ACT, 4, 2, 4, 2>(a, s);
+  if (a.rows <= 16) return rows_go<ACT, 1, 2, 8, 4, 2>(a, s);
+  if (a.rows <= 32) return rows_go<ACT, 2, 2, 8, 2, 1>(a, s);
+  if (a.rows <= 64) return rows_go<ACT, 4, 3, 4, 2, 1>(a, s);
   const long long grid = (long long)((a.tiles + kTileN / 16 - 1) / (kTileN / 16)) * ((a.rows + kTileM - 1) / kTileM);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((k_linear_tile<ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);

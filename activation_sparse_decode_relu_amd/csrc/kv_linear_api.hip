@@ -14,6 +14,7 @@ using pik::fail;
 using pik::ok;
 
 constexpr int kMaxIn = 1 << 20, kMaxOut = 1 << 24, kMaxRows = 1 << 24;
+constexpr int kMaxStride = 1 << 23;   // 128 rows' offsets in bytes fit in 32 bits
 constexpr uintptr_t kAlign = 256;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -91,8 +92,8 @@ pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stre
   if (args->x == nullptr || !aligned(args->x, 16)) return fail(PI_ERR_INVALID, "x is NULL or not 16-byte aligned");
   if (args->y == nullptr || !aligned(args->y, 2)) return fail(PI_ERR_INVALID, "y is NULL or not 2-byte aligned");
   if (!aligned(args->add, 2)) return fail(PI_ERR_INVALID, "add is not 2-byte aligned");
-  if (args->rows > 1 && (args->x_stride < 0 || args->x_stride % 8 != 0))
-    return fail(PI_ERR_INVALID, "x_stride=%lld must be a non-negative multiple of 8 elements", (long long)args->x_stride);
+  if (args->rows > 1 && (args->x_stride < 0 || args->x_stride % 8 != 0 || args->x_stride > kMaxStride))
+    return fail(PI_ERR_INVALID, "x_stride=%lld must be a multiple of 8 elements in [0, 2^23]", (long long)args->x_stride);
   if (args->rows > 1 && args->add != nullptr && args->add_stride < 0)
     return fail(PI_ERR_INVALID, "add_stride=%lld must not be negative", (long long)args->add_stride);
   if (args->rows > 1 && args->y_stride < d.d_out)
@@ -103,7 +104,7 @@ pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stre
   a.x = args->x;
   a.add = args->add;
   a.y = args->y;
-  a.x_stride = args->x_stride;
+  a.x_stride = args->rows > 1 ? args->x_stride : 0;
   a.add_stride = args->add_stride;
   a.y_stride = args->y_stride;
   a.rows = args->rows;

@@ -49,7 +49,7 @@ typedef struct pi_linear_args {
   const void* x;      /* [rows][d_in], 16-byte aligned                                      */
   const void* add;    /* [rows][d_out] or NULL                                              */
   void* y;            /* [rows][d_out]                                                      */
-  int64_t x_stride;   /* from row to row, in elements: a multiple of 8 (looked at for several rows) */
+  int64_t x_stride;   /* from row to row, in elements: a multiple of 8 up to 2^23 (looked at for several rows) */
   int64_t add_stride; /* in elements                                                        */
   int64_t y_stride;   /* in elements, at least d_out                                        */
   int32_t rows;       /* 0 to 2^24; 0 enqueues nothing                                      */

@@ -92,7 +92,7 @@ class _Handle:
 
 
 @pytest.mark.parametrize("change", [dict(rows=-1), dict(rows=(1 << 24) + 1), dict(x=None), dict(x=FAKE + 8), dict(y=None),
-                                    dict(y=FAKE + 1), dict(add=FAKE + 1), dict(x_stride=68), dict(x_stride=-64),
+                                    dict(y=FAKE + 1), dict(add=FAKE + 1), dict(x_stride=68), dict(x_stride=-64), dict(x_stride=(1 << 23) + 8),
                                     dict(add=FAKE, add_stride=-8), dict(y_stride=7)])
 def test_forward_refusals(change):
     assert _Handle(64, 8).forward(**change) == 1 and pi.last_error()
