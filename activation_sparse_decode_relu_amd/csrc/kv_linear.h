@@ -12,6 +12,7 @@ constexpr int kSlabRows = 16, kSlabCols = 256, kSlabBytes = 2304;
 
 struct LinearArgs {
   const uint8_t* packed;   // [tiles][slabs][kSlabBytes]
+  const float* factor;     // [tiles * 16]: powers of two that the rows' scales were divided by
   const float* bias;       // [d_out] or NULL
   const void* x;
   const void* add;         // or NULL
@@ -21,7 +22,8 @@ struct LinearArgs {
   int tiles, slabs;
 };
 
-hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, int d_in, int d_out, hipStream_t s);
+hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
+                              hipStream_t s);
 hipError_t launch_linear(int act, const LinearArgs& a, hipStream_t s);
 
 }  // namespace pik

@@ -50,11 +50,27 @@ __device__ __forceinline__ typename ActT<ACT>::V8 operand(unsigned w, unsigned o
 
 // ---- laying out ----------------------------------------------------------------------------------------
 
+// One wave a row of scales: the power of two that brings the largest to [8, 16).  So products of codes and scales stay in
+// fp16's normal range whatever the row's size is.
+__global__ __launch_bounds__(256) void k_linear_factor(const unsigned short* __restrict__ scales, float* __restrict__ factor,
+                                                       int groups, int d_out, int padded) {
+  const int row = blockIdx.x * (256 / WAVE) + threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+  if (row >= padded) return;
+  float top = 0.0f;
+  if (row < d_out)
+    for (int k = lane; k < groups; k += WAVE)
+      top = fmaxf(top, fabsf((float)__builtin_bit_cast(f16, scales[(size_t)row * groups + k])));
+#pragma unroll
+  for (int m = 1; m < WAVE; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+  const int x = (int)(__builtin_bit_cast(unsigned, top) >> 23) - 127;   // top in [2^x, 2^(x + 1)), exact in fp32
+  if (lane == 0) factor[row] = top > 0.0f && top <= 65504.0f ? pow2i(x - 3) : 1.0f;
+}
+
 // One wave a slab.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__ w, const unsigned short* __restrict__ scales,
-                                                     uint8_t* __restrict__ packed, int d_in, int d_out, int slabs,
-                                                     long long count) {
+                                                     uint8_t* __restrict__ packed, const float* __restrict__ factor, int d_in,
+                                                     int d_out, int slabs, long long count) {
   const long long at = (long long)blockIdx.x * (256 / WAVE) + threadIdx.x / WAVE;
   if (at >= count) return;
   const int lane = threadIdx.x & (WAVE - 1), slab = (int)(at % slabs);
@@ -83,7 +99,10 @@ __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int group = slab * 8 + 2 * (lane % 4) + e;
-    if (srow < d_out && group < d_in / 32) s |= (unsigned)scales[(size_t)srow * (d_in / 32) + group] << (16 * e);
+    if (srow < d_out && group < d_in / 32) {
+      const float scale = (float)__builtin_bit_cast(f16, scales[(size_t)srow * (d_in / 32) + group]);
+      s |= (unsigned)__builtin_bit_cast(unsigned short, (f16)(scale / factor[srow])) << (16 * e);
+    }
   }
   *reinterpret_cast<unsigned*>(to + 2048 + lane * 4) = s;
 }
@@ -166,6 +185,7 @@ __device__ __forceinline__ void join_waves(const LinearArgs& A, float* s_part, c
     const int at = (((k % (16 * T) / 16) * NB + b) * NI + i) * WAVE + 16 * q + k % 16;
     float v = s_part[at];
     for (int w = 1; w < waves; ++w) v += s_part[w * kSums + at];
+    v *= A.factor[n];
     if (A.bias != nullptr) v += A.bias[n];
     if (A.add != nullptr) v += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
     static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)v;
@@ -247,7 +267,8 @@ __device__ __forceinline__ unsigned stage_byte(int col, int end) {
   const int lane = threadIdx.x & (WAVE - 1);
   return 2u * (unsigned)min(col + 8 * ((lane ^ (lane >> 3)) & 7), end - 8);
 }
-// 16 bytes a lane from base + at to LDS, lane after lane.
+// 16 bytes a lane from base + at to LDS, lane after lane.  (To the compiler they are words: LDS is read as vectors, for which
+// it does not wait.)
 __device__ __forceinline__ void bring(const void* base, unsigned at, void* to) {
   const auto* from = reinterpret_cast<const __attribute__((address_space(1))) char*>(reinterpret_cast<uintptr_t>(base));
   __builtin_amdgcn_global_load_lds(reinterpret_cast<const __attribute__((address_space(1))) unsigned*>(from + at),
@@ -259,12 +280,14 @@ __device__ __forceinline__ V8 x_operand(const V8 (&x)[16][kStage / 8], int k) {
   const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
   return x[r][(4 * k + (lane >> 4)) ^ (r & 7)];
 }
-// At most N of this wave's loads are still on their way.
-template <int N>
+// At most N of this wave's loads are still on their way, and L of its LDS operations (15: any number).  (The builtin, since
+// the compiler adds waits of its own where it does not know of one.)
+template <int N, int L = 15>
 __device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0f70);
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070 | L << 8);
   asm volatile("" ::: "memory");
 }
+template <int N> struct Count { static constexpr int value = N; };
 
 // Up to 16 NB rows; T tiles a workgroup, whose waves take the slabs in turn.  Each wave brings the x of its own slabs to
 // LDS, DEPTH - 1 stages of 64 columns ahead; codes come PRE slabs ahead.
@@ -364,8 +387,12 @@ out:
 
 // ---- more than 64 rows ---------------------------------------------------------------------------------
 
-// Bound by the vector ALU (an fp32 multiply-add for each output and group, as long as the product itself) and the matrix
-// instructions.  A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x, codes and scales go to LDS
+// Bound by issue: on this hardware a wave's vector ALU instruction runs beside a matrix instruction only in part (a
+// 16x16x32 one and n others take 15.6 + 3.7 n cycles together, a 32x32x16 one, twice the work, 19 + 3.9 n).  With an fp32
+// multiply-add for each output and group, as many cycles as the product itself, 2000 rows 4096 -> 12288 took 328 us.  So
+// with fp16 activations code times scale is an fp16 operand, rounded to half a step of 2^-11 (as much as y itself), and the
+// sums stay in the matrix instructions.  There is no packed arithmetic in bf16, whose operands stay whole numbers.
+// A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x, codes and scales go to LDS
 // without passing registers: x in stages of 64 columns, two ahead of the one in use, codes two stages ahead too.
 constexpr int kTileM = 128, kTileN = 128;
 template <int ACT>
@@ -378,7 +405,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
   u32x4(*s_code)[kTiles][WAVE] = reinterpret_cast<u32x4(*)[kTiles][WAVE]>(s_mem + kRing * kTileM * kStage * 2);
   u32x4(*s_scale)[4][WAVE] = reinterpret_cast<u32x4(*)[4][WAVE]>(s_mem + kRing * kTileM * kStage * 2 + 2 * kTiles * 1024);
   const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  const int g = lane >> 4, wm = wave >> 1, wn = wave & 1;
+  const int wm = wave >> 1, wn = wave & 1;
   const int across = (A.tiles + kTiles - 1) / kTiles;
   const int row0 = (int)(blockIdx.x / across) * kTileM, tile0 = (int)(blockIdx.x % across) * kTiles;
   const E* x0 = static_cast<const E*>(A.x) + (int64_t)row0 * A.x_stride;
@@ -408,88 +435,149 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
     const uint8_t* p = from[0] + (size_t)min(slab, A.slabs - 1) * kSlabBytes + 2048;
     bring(p, 16u * (lane & 15) + (lane & 16 ? (unsigned)(from[1] - from[0]) : 0u), &s_scale[slot][wave][0]);
   };
+  // kFold: 2 x 2 tiles of 32 x 32, operands 2 t + m for columns 16 m .. of a group of tile t; else 4 x 4 of 16 x 16
+  constexpr bool kFold = ACT == ACT_F16;
+  const int c = kFold ? lane & 31 : lane & 15, part = kFold ? lane >> 5 : lane >> 4;   // this lane's row of x or W, and columns
+  typedef float f32x16 __attribute__((ext_vector_type(16)));
+  f32x16 sum[2][2];
   float acc[4][4][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[j][b][i] = 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        acc[j][b][i] = 0.0f;
+        sum[j / 2][b / 2][8 * (j % 2) + 4 * (b % 2) + i] = 0.0f;
+      }
   const V8 minus = minus24<ACT>();
   const unsigned one = sixteen<ACT>();
   Late<4> late;
-  u32x4 code[4], scale[4];
+  u32x2 code[2][4];      // of the stage at hand and the next one: a word for each of its two groups
+  f16x2 scale[2][4];     // and scale
+  V8 v[2][4];            // of the group at hand and the next one
+  auto read_x = [&](int slot, int k, V8 (&to)[4]) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int tile = kFold ? 4 * wm + 2 * (b / 2) + (c >> 4) : 4 * wm + b, chunk = kFold ? 2 * (b % 2) + part : part;
+      to[b] = s_x[slot][tile][c & 15][(4 * k + chunk) ^ (c & 7)];
+    }
+  };
+  auto read_codes = [&](int slab, int q, u32x2 (&to)[4], f16x2 (&scales)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int tile = kFold ? 4 * wn + 2 * (j / 2) + (c >> 4) : 4 * wn + j, chunk = kFold ? 2 * (j % 2) + part : part;
+      to[j] = *(reinterpret_cast<const u32x2*>(&s_code[q / 2][tile][16 * chunk + (c & 15)]) + q % 2);
+      if (!kFold || j % 2 == 0)
+        scales[j] = *(reinterpret_cast<const f16x2*>(&s_scale[slab & 1][tile / 2][16 * (tile % 2) + (c & 15)]) + q);
+    }
+  };
+  auto group = [&](const V8 (&x)[4], const u32x2 (&code)[4], const f16x2 (&scale)[4], int k) {
+    if constexpr (kFold) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f16x2 by = {scale[j & ~1][k], scale[j & ~1][k]}, less = {(f16)24.0f, (f16)24.0f};
+        const V8 raw = operand<ACT>(code[j][k], one);
+        V8 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const f16x2 y = (f16x2{raw[2 * e], raw[2 * e + 1]} - less) * by;   // the difference is exact
+          w[2 * e] = y.x;
+          w[2 * e + 1] = y.y;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) sum[j / 2][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[2 * b + j % 2], w, sum[j / 2][b], 0, 0, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+      }
+    } else {
+      f32x4 c[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) c[b] = product<ACT>(x[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
+      late.add(acc[3]);
+      interleave<4>();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const V8 w = operand<ACT>(code[j][k], one);
+        f32x4 now[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) now[b] = product<ACT>(x[b], w, c[b]);
+        if (j > 0) late.add(acc[j - 1]);
+        late.set(now, (float)scale[j][k]);
+        interleave<4>();
+      }
+    }
+  };
+  // Wait until all but the last N loads are there, for every wave.  (Not __syncthreads(), which waits for all of them; the
+  // operands read so far are there too.)
+  auto meet = [&](auto n) {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_loads<decltype(n)::value, 0>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
   bring_x(0, 0);
   bring_codes(0, 0);
   bring_scales(0, 0);
   bring_x(1, 1);
+  bring_x(2, 2);
+  bring_codes(1, 1);
+  meet(Count<10>{});
+  read_x(0, 0, v[0]);
+  read_codes(0, 0, code[0], scale[0]);
   int slot = 0;   // stage % kRing
   for (int slab = 0; slab < A.slabs; ++slab) {
 #pragma unroll
-    for (int q = 0; q < kSlabCols / kStage; ++q) {
-      const int stage = slab * (kSlabCols / kStage) + q;
-      // what was asked for two stages ago is there; behind it is what the last stage asked for
-      if (q == 1) wait_loads<6>();
-      else if (q == 3) wait_loads<7>();
-      else wait_loads<4>();
-      // (not __syncthreads(), which waits for all that is on its way; every operand read so far has been used)
-      __builtin_amdgcn_s_barrier();
+    for (int q = 0; q < 4; ++q) {
+      const int stage = 4 * slab + q, after = slot == kRing - 1 ? 0 : slot + 1;
+      read_x(slot, 1, v[1]);
+      group(v[0], code[q % 2], scale[q % 2], 0);
+      // the next stage is there when all that was asked for before the last stage's half is; this stage has been read
+      if (q == 0) meet(Count<6>{});
+      else if (q == 2) meet(Count<7>{});
+      else meet(Count<4>{});
+      bring_x(stage + 3, slot);
+      if (q % 2 == 1) bring_codes(2 * slab + (q + 3) / 2, ((q + 3) / 2) % 2);
+      if (q == 1) bring_scales(slab + 1, (slab + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
-      const int ahead = slot >= 1 ? slot - 1 : kRing - 1;
-      bring_x(stage + 2, ahead);
-      if (q % 2 == 0) bring_codes(2 * slab + q / 2 + 1, (q / 2 + 1) % 2);
-      if (q == 2) bring_scales(slab + 1, (slab + 1) & 1);
+      read_x(after, 0, v[0]);
+      read_codes(slab + (q + 1) / 4, (q + 1) % 4, code[(q + 1) % 2], scale[(q + 1) % 2]);
+      group(v[1], code[q % 2], scale[q % 2], 1);
       __builtin_amdgcn_sched_barrier(0);
-      if (q == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) scale[j] = s_scale[slab & 1][2 * wn + j / 2][16 * (j % 2) + (lane & 15)];
-      }
-      if (q % 2 == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code[j] = s_code[q / 2][4 * wn + j][lane];
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        V8 v[4];
-        f32x4 c[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          v[b] = x_operand(s_x[slot][4 * wm + b], k);
-          c[b] = product<ACT>(v[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const V8 w = operand<ACT>(code[j][2 * (q % 2) + k], one);
-          const int group = 2 * q + k;
-          f32x4 now[4];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) now[b] = product<ACT>(v[b], w, c[b]);
-          late.add(acc[(j + 3) % 4]);
-          late.set(now, (float)as_h2(scale[j][group / 2])[group % 2]);
-          interleave<4>();
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      slot = slot == kRing - 1 ? 0 : slot + 1;
+      slot = after;
     }
   }
-  late.add(acc[3]);
+  if constexpr (!kFold) late.add(acc[3]);
   wait_loads<0>();   // nothing is on its way to LDS when the workgroup ends
+  // Four rows of an output: rows r .. r + 3 of this wave's 64.
+  auto store4 = [&](int r, int n, float factor, float bias, const float (&sums)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int n = (tile0 + 4 * wn + j) * 16 + (lane & 15);
-    if (n >= A.d_out) continue;
-    const float bias = A.bias != nullptr ? A.bias[n] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const int t = row0 + 64 * wm + r + i;
+      if (t >= A.rows || n >= A.d_out) continue;
+      float y = fmaf(sums[i], factor, bias);
+      if (A.add != nullptr) y += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
+      static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)y;
+    }
+  };
+  constexpr int kWide = kFold ? 32 : 16, kEach = 64 / kWide;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+  for (int j = 0; j < kEach; ++j) {
+    const int n = (tile0 + 4 * wn) * 16 + j * kWide + c, at = min(n, A.d_out - 1);
+    const float factor = A.factor[at], bias = A.bias != nullptr ? A.bias[at] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = row0 + 64 * wm + 16 * b + 4 * g + i;
-        if (t >= A.rows) continue;
-        float y = acc[j][b][i] + bias;
-        if (A.add != nullptr) y += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
-        static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)y;
+    for (int b = 0; b < kEach; ++b) {
+      if constexpr (kFold) {
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+          store4(32 * b + 8 * a + 4 * part, n, factor, bias,
+                 {sum[j][b][4 * a], sum[j][b][4 * a + 1], sum[j][b][4 * a + 2], sum[j][b][4 * a + 3]});
+      } else {
+        store4(16 * b + 4 * part, n, factor, bias, {acc[j][b][0], acc[j][b][1], acc[j][b][2], acc[j][b][3]});
       }
+    }
   }
 }
 
@@ -523,16 +611,24 @@ hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, int d_in, int d_out, hipStream_t s) {
-  const int slabs = (d_in + kSlabCols - 1) / kSlabCols;
-  const long long count = (long long)((d_out + kSlabRows - 1) / kSlabRows) * slabs, grid = (count + 3) / 4;
+hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
+                              hipStream_t s) {
+  const int slabs = (d_in + kSlabCols - 1) / kSlabCols, tiles = (d_out + kSlabRows - 1) / kSlabRows;
+  const long long count = (long long)tiles * slabs, grid = (count + 3) / 4;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const auto* codes = static_cast<const uint8_t*>(w);
+  const auto* halves = static_cast<const unsigned short*>(scales);
+  auto* to = static_cast<uint8_t*>(packed);
+  hipLaunchKernelGGL(k_linear_factor, dim3((unsigned)(tiles * kSlabRows + 3) / 4), dim3(256), 0, s, halves, factor, d_in / 32,
+                     d_out, tiles * kSlabRows);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (act == ACT_F16)
-    hipLaunchKernelGGL((k_linear_pack<ACT_F16>), dim3((unsigned)grid), dim3(256), 0, s, static_cast<const uint8_t*>(w),
-                       static_cast<const unsigned short*>(scales), static_cast<uint8_t*>(packed), d_in, d_out, slabs, count);
+    hipLaunchKernelGGL((k_linear_pack<ACT_F16>), dim3((unsigned)grid), dim3(256), 0, s, codes, halves, to, factor, d_in, d_out,
+                       slabs, count);
   else
-    hipLaunchKernelGGL((k_linear_pack<ACT_BF16>), dim3((unsigned)grid), dim3(256), 0, s, static_cast<const uint8_t*>(w),
-                       static_cast<const unsigned short*>(scales), static_cast<uint8_t*>(packed), d_in, d_out, slabs, count);
+    hipLaunchKernelGGL((k_linear_pack<ACT_BF16>), dim3((unsigned)grid), dim3(256), 0, s, codes, halves, to, factor, d_in, d_out,
+                       slabs, count);
   return hipGetLastError();
 }
 

@@ -21,7 +21,8 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 
 int tiles_of(const pi_linear_desc& d) { return (d.d_out + pik::kSlabRows - 1) / pik::kSlabRows; }
 int slabs_of(const pi_linear_desc& d) { return (d.d_in + pik::kSlabCols - 1) / pik::kSlabCols; }
-size_t packed_of(const pi_linear_desc& d) { return (size_t)tiles_of(d) * slabs_of(d) * pik::kSlabBytes; }
+size_t slabs_bytes(const pi_linear_desc& d) { return (size_t)tiles_of(d) * slabs_of(d) * pik::kSlabBytes; }
+size_t packed_of(const pi_linear_desc& d) { return slabs_bytes(d) + (size_t)tiles_of(d) * pik::kSlabRows * sizeof(float); }
 
 pi_status check_desc(const pi_linear_desc* d) {
   if (d == nullptr) return fail(PI_ERR_INVALID, "desc is NULL");
@@ -39,6 +40,8 @@ struct pi_linear {
   pi_linear_desc desc;
   const uint8_t* packed;
   const float* bias;
+
+  const float* factor() const { return reinterpret_cast<const float*>(packed + slabs_bytes(desc)); }
 };
 
 extern "C" {
@@ -67,8 +70,8 @@ pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void
     return fail(PI_ERR_WORKSPACE, "packed must be %zu bytes, %zu-byte aligned", need, (size_t)kAlign);
   pi_linear* h = new (std::nothrow) pi_linear{*desc, static_cast<const uint8_t*>(packed), bias};
   if (h == nullptr) return fail(PI_ERR_INVALID, "out of host memory");
-  const hipError_t e = pik::launch_linear_pack(desc->act_dtype, w, scales, packed, desc->d_in, desc->d_out,
-                                               static_cast<hipStream_t>(stream));
+  const hipError_t e = pik::launch_linear_pack(desc->act_dtype, w, scales, packed, const_cast<float*>(h->factor()), desc->d_in,
+                                               desc->d_out, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) {
     delete h;
     return fail(PI_ERR_HIP, "laying the weights out failed: %s", hipGetErrorString(e));
@@ -100,6 +103,7 @@ pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stre
     return fail(PI_ERR_INVALID, "y_stride=%lld is less than d_out=%d", (long long)args->y_stride, d.d_out);
   pik::LinearArgs a{};
   a.packed = h->packed;
+  a.factor = h->factor();
   a.bias = h->bias;
   a.x = args->x;
   a.add = args->add;

@@ -13,15 +13,18 @@
  * [ceil(d_out / 16)][ceil(d_in / 256)] slabs of 2304 bytes: two KB of codes, one for each 128 columns, and fp16
  * scales [16 rows][8 groups].  Word j of the 16 bytes 16 l .. of a KB holds the columns 32 j + 8 (l / 16) .. + 8
  * of row l % 16, as u = q + 8: column 2 i at bit 4 i and column 2 i + 1 at bit 16 + 4 i, the word rotated left
- * by 6 bits (fp16 activations) or 3 (bf16).  Rows and columns that are not there have q = 0 and scale 0.
+ * by 6 bits (fp16 activations) or 3 (bf16).  Rows and columns that are not there have q = 0 and scale 0.  Behind the
+ * slabs stands a power of two for each row (fp32) that its scales were divided by, which brings the largest of them to
+ * [8, 16); what a scale 2^-17 of that and less loses lies under the sums' own rounding.
  *
  * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
  * --------------------------------------------------------------------------------------------------
  * - Ownership: the caller allocates all device memory; a handle borrows it until pi_linear_destroy.
  * - Streams: calls only enqueue on `stream`.  A handle has no workspace: its calls may run at the same time.
  * - Products of whole numbers and activations are summed in fp32 by groups of 32, and the groups' sums, times
- *   their scales, in fp32; y is rounded once.  A row's result depends on its own x, and, in its last bits, on
- *   the number of rows of the call; it does not depend on the order in which workgroups run.
+ *   their scales, in fp32; y is rounded once.  With fp16 activations and more than 64 rows, code times scale is
+ *   rounded to fp16 (half a step of 2^-11) and summed in fp32.  A row's result depends on its own x, and, in its last
+ *   bits, on the number of rows of the call; it does not depend on the order in which workgroups run.
  * - A row of x that holds an infinity, a NaN, or (bf16) a magnitude of 2^118 and more may come out as NaN, other
  *   rows are not touched by it.
  */

@@ -3,7 +3,9 @@
 Bounds.  A group's sum is a product of whole numbers 24 + q with x, begun with -24 sum x, itself summed in fp32: 32 terms
 of at most 24 |x| and 33 of at most 55 of the group's sum |x| (the beginning among them), each addition off by 2^-24:
 (32 * 24 + 33 * 55) 2^-24 < 2600 * 2^-24 of it, times the scale.  The G groups, the waves, bias and add join in fp32:
-(G + 12) 2^-24 of the terms' magnitudes.  y is rounded once: half a step of its type.
+(G + 12) 2^-24 of the terms' magnitudes.  y is rounded once: half a step of its type.  With fp16 and more than 64 rows a
+weight is rounded to fp16, relative to the row's largest scale in [8, 16): half a step, 2^-11 of it, or 2^-25 / 8 of that
+scale where that is more; and scales of less than 2^-17 of the largest lose as little, times 8.
 """
 
 import numpy as np
@@ -55,6 +57,9 @@ class Rig:
         mass = np.abs(x) @ np.abs(self.w).T + np.abs(bias) + np.abs(more)
         tol = (2600 * 2.0 ** -24 * (np.abs(x) @ self.s.T) + (self.d_in // 32 + 12) * 2.0 ** -24 * mass +
                EPS[self.act] * np.abs(ref) + TINY[self.act])
+        tol += 2.0 ** -25 * (np.abs(x).sum(1, keepdims=True) * self.s.max(1))          # scales kept relative to the row's largest
+        if self.act == "f16" and x.shape[0] > 64:
+            tol += 2.0 ** -11 * (np.abs(x) @ np.abs(self.w).T) * (1 + EPS[self.act])
         err = np.abs(y.double().cpu().numpy() - ref)
         assert np.all(err <= tol), f"off by {np.max(err / tol):.2f} times its bound"
 
@@ -126,7 +131,7 @@ def test_strides_and_what_lies_beside(rows):
 
 @pytest.mark.parametrize("act", ["f16", "bf16"])
 def test_a_row_does_not_touch_another(act):
-    """Rows with infinities and NaN are NaN, the others keep their bits; the order of rows does not matter."""
+    """Rows with infinities and NaN are not finite, the others keep their bits; the order of rows does not matter."""
     announce(f"linear rows apart {act}")
     for rows in (2, 4, 13, 40, 70):
         r = Rig(512, 48, act, seed=rows)
@@ -136,7 +141,7 @@ def test_a_row_does_not_touch_another(act):
         bad = x.clone()
         bad[1, 3], bad[0, 100] = float("inf"), float("nan")
         r.m.forward(bad, z)
-        assert bool(z[:2].isnan().all()) and torch.equal(z[2:], y[2:])
+        assert not bool(z[:2].isfinite().any()) and torch.equal(z[2:], y[2:])
         r.m.forward(x.flip(0).contiguous(), z)
         assert torch.equal(z.flip(0), y)
 

@@ -42,7 +42,7 @@ def test_struct_layouts():
 
 @pytest.mark.parametrize("d_in, d_out, tiles, slabs", [(32, 1, 1, 1), (256, 16, 1, 1), (288, 17, 2, 2), (8192, 10240, 640, 32)])
 def test_packed_bytes(d_in, d_out, tiles, slabs):
-    assert pi.linear_packed_bytes(pi.linear_desc(d_in, d_out)) == tiles * slabs * 2304
+    assert pi.linear_packed_bytes(pi.linear_desc(d_in, d_out)) == tiles * slabs * 2304 + 64 * tiles
 
 
 @pytest.mark.parametrize("bad", [dict(d_in=0), dict(d_in=48), dict(d_in=-32), dict(d_in=(1 << 20) + 32), dict(d_out=0),
@@ -62,9 +62,9 @@ def test_numbers_past_32_bits():
 
 @pytest.mark.parametrize("change, status", [
     (dict(w=None), 1), (dict(w=FAKE + 2), 1), (dict(scales=None), 1), (dict(scales=FAKE + 1), 1), (dict(bias=FAKE + 2), 1),
-    (dict(packed=None), 2), (dict(packed=FAKE + 16), 2), (dict(size=2303), 2)])
+    (dict(packed=None), 2), (dict(packed=FAKE + 16), 2), (dict(size=2304 + 63), 2)])
 def test_create_refusals(change, status):
-    a = {**dict(w=FAKE, scales=FAKE, bias=None, packed=FAKE, size=2304), **change}
+    a = {**dict(w=FAKE, scales=FAKE, bias=None, packed=FAKE, size=2304 + 64), **change}
     d, h = pi.linear_desc(64, 8), ctypes.c_void_p()
     st = pi.LIB.pi_linear_create(ctypes.byref(d), a["w"], a["scales"], a["bias"], a["packed"], a["size"], None, ctypes.byref(h))
     assert st == status and not h.value
