@@ -393,17 +393,18 @@ out:
 // with fp16 activations code times scale is an fp16 operand, rounded to half a step of 2^-11 (as much as y itself), and the
 // sums stay in the matrix instructions.  There is no packed arithmetic in bf16, whose operands stay whole numbers.
 // A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x, codes and scales go to LDS
-// without passing registers: x in stages of 64 columns, two ahead of the one in use, codes two stages ahead too.
+// without passing registers: x in stages of 64 columns, one and a half ahead of the one in use, codes three.  Two buffers
+// and no more, so that three workgroups fit in a compute unit.
 constexpr int kTileM = 128, kTileN = 128;
 template <int ACT>
 __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
   using E = typename ActT<ACT>::T;
   using V8 = typename ActT<ACT>::V8;
-  constexpr int kTiles = kTileN / 16, kRing = 3;
-  __shared__ __align__(16) char s_mem[kRing * kTileM * kStage * 2 + 2 * kTiles * 1024 + 2 * 4 * 1024];
+  constexpr int kTiles = kTileN / 16, kRing = 2;
+  __shared__ __align__(16) char s_mem[kRing * kTileM * kStage * 2 + 2 * kTiles * 1024 + 2 * kTiles * 256];
   XTile<V8>(*s_x)[kTileM / 16] = reinterpret_cast<XTile<V8>(*)[kTileM / 16]>(s_mem);
   u32x4(*s_code)[kTiles][WAVE] = reinterpret_cast<u32x4(*)[kTiles][WAVE]>(s_mem + kRing * kTileM * kStage * 2);
-  u32x4(*s_scale)[4][WAVE] = reinterpret_cast<u32x4(*)[4][WAVE]>(s_mem + kRing * kTileM * kStage * 2 + 2 * kTiles * 1024);
+  u32x4(*s_scale)[kTiles][16] = reinterpret_cast<u32x4(*)[kTiles][16]>(s_mem + kRing * kTileM * kStage * 2 + 2 * kTiles * 1024);
   const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int wm = wave >> 1, wn = wave & 1;
   const int across = (A.tiles + kTiles - 1) / kTiles;
@@ -431,9 +432,11 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
     for (int e = 0; e < 2; ++e)
       bring(from[e] + (size_t)(p / 2) * kSlabBytes + 1024 * (p % 2), 16u * lane, &s_code[slot][2 * wave + e][0]);
   };
-  auto bring_scales = [&](int slab, int slot) {   // rows lane % 16 of the two tiles, twice
-    const uint8_t* p = from[0] + (size_t)min(slab, A.slabs - 1) * kSlabBytes + 2048;
-    bring(p, 16u * (lane & 15) + (lane & 16 ? (unsigned)(from[1] - from[0]) : 0u), &s_scale[slot][wave][0]);
+  const unsigned scale_at =   // four tiles a wave, and twice, so that every wave has asked for as many loads
+      (unsigned)(min(tile0 + 4 * (wave & 1) + (lane >> 4), A.tiles - 1) - tile0) * (unsigned)tile_bytes + 2048u + 16u * (lane & 15);
+  auto bring_scales = [&](int slab, int slot) {
+    bring(A.packed + (size_t)tile0 * tile_bytes + (size_t)min(slab, A.slabs - 1) * kSlabBytes, scale_at,
+          &s_scale[slot][4 * (wave & 1)][0]);
   };
   // kFold: 2 x 2 tiles of 32 x 32, operands 2 t + m for columns 16 m .. of a group of tile t; else 4 x 4 of 16 x 16
   constexpr bool kFold = ACT == ACT_F16;
@@ -469,7 +472,7 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
       const int tile = kFold ? 4 * wn + 2 * (j / 2) + (c >> 4) : 4 * wn + j, chunk = kFold ? 2 * (j % 2) + part : part;
       to[j] = *(reinterpret_cast<const u32x2*>(&s_code[q / 2][tile][16 * chunk + (c & 15)]) + q % 2);
       if (!kFold || j % 2 == 0)
-        scales[j] = *(reinterpret_cast<const f16x2*>(&s_scale[slab & 1][tile / 2][16 * (tile % 2) + (c & 15)]) + q);
+        scales[j] = *(reinterpret_cast<const f16x2*>(&s_scale[slab & 1][tile][c & 15]) + q);
     }
   };
   auto group = [&](const V8 (&x)[4], const u32x2 (&code)[4], const f16x2 (&scale)[4], int k) {
@@ -521,45 +524,49 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
   bring_x(0, 0);
   bring_codes(0, 0);
   bring_scales(0, 0);
+  __builtin_amdgcn_sched_barrier(0);
   bring_x(1, 1);
-  bring_x(2, 2);
+  __builtin_amdgcn_sched_barrier(0);
   bring_codes(1, 1);
-  meet(Count<10>{});
+  meet(Count<6>{});
   read_x(0, 0, v[0]);
   read_codes(0, 0, code[0], scale[0]);
-  int slot = 0;   // stage % kRing
   for (int slab = 0; slab < A.slabs; ++slab) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int stage = 4 * slab + q, after = slot == kRing - 1 ? 0 : slot + 1;
-      read_x(slot, 1, v[1]);
+      const int stage = 4 * slab + q;
+      read_x(q % 2, 1, v[1]);
       group(v[0], code[q % 2], scale[q % 2], 0);
-      // the next stage is there when all that was asked for before the last stage's half is; this stage has been read
-      if (q == 0) meet(Count<6>{});
-      else if (q == 2) meet(Count<7>{});
-      else meet(Count<4>{});
-      bring_x(stage + 3, slot);
+      // this stage has been read, and the next one is there, if not yet the codes that were asked for after it
+      if (q == 0) meet(Count<2>{});
+      else if (q == 2) meet(Count<3>{});
+      else meet(Count<0>{});
+      bring_x(stage + 2, q % 2);
+      __builtin_amdgcn_sched_barrier(0);
       if (q % 2 == 1) bring_codes(2 * slab + (q + 3) / 2, ((q + 3) / 2) % 2);
       if (q == 1) bring_scales(slab + 1, (slab + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
-      read_x(after, 0, v[0]);
+      read_x((q + 1) % 2, 0, v[0]);
       read_codes(slab + (q + 1) / 4, (q + 1) % 4, code[(q + 1) % 2], scale[(q + 1) % 2]);
       group(v[1], code[q % 2], scale[q % 2], 1);
       __builtin_amdgcn_sched_barrier(0);
-      slot = after;
     }
   }
   if constexpr (!kFold) late.add(acc[3]);
   wait_loads<0>();   // nothing is on its way to LDS when the workgroup ends
   // Four rows of an output: rows r .. r + 3 of this wave's 64.
+  const int left = A.rows - row0 - 64 * wm;
+  const E* add0 = static_cast<const E*>(A.add) + (int64_t)(row0 + 64 * wm) * A.add_stride;
+  E* y0 = static_cast<E*>(A.y) + (int64_t)(row0 + 64 * wm) * A.y_stride;
   auto store4 = [&](int r, int n, float factor, float bias, const float (&sums)[4]) {
+    const E* add = add0 + (int64_t)r * A.add_stride + n;
+    E* y = y0 + (int64_t)r * A.y_stride + n;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = row0 + 64 * wm + r + i;
-      if (t >= A.rows || n >= A.d_out) continue;
-      float y = fmaf(sums[i], factor, bias);
-      if (A.add != nullptr) y += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
-      static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)y;
+      if (r + i >= left || n >= A.d_out) continue;
+      float v = fmaf(sums[i], factor, bias);
+      if (A.add != nullptr) v += (float)add[i * A.add_stride];
+      y[i * A.y_stride] = (E)v;
     }
   };
   constexpr int kWide = kFold ? 32 : 16, kEach = 64 / kWide;
