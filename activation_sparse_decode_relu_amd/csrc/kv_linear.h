@@ -20,9 +20,41 @@ struct LinearArgs {
   int64_t x_stride, add_stride, y_stride;
   int rows, d_in, d_out;
   int tiles, slabs;
+  void* scratch;             // as linear_scratch() lays it out
+  const float* row_factor;   // set by the launch: powers of two that rows of x were divided by, or NULL
+  float* partial;            // set by the launch: [splits][rows][d_out]
+  int splits;                // set by the launch: ranges of slabs
 };
 
-hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
+// Up to kExactRows rows x stays in its type.  More are taken in tiles of kTileM rows and kTileTiles tiles of outputs; where
+// these leave the card with too few workgroups, the slabs are split over up to kMostSplits, each of at least two.
+constexpr int kExactRows = 64, kTileM = 128, kTileTiles = 8, kMostSplits = 8, kLinearGroups = 512;
+struct LinearScratch {
+  size_t x, factor, partial, total;   // fp16 rows and their factors (bf16 alone), the ranges' sums
+  int splits;
+};
+inline LinearScratch linear_scratch(int act, int rows, int d_in, int d_out) {
+  LinearScratch l{};
+  l.splits = 1;
+  if (rows <= kExactRows) return l;
+  auto align = [](size_t v) { return (v + 255) / 256 * 256; };
+  if (act != 0) {
+    l.factor = align((size_t)rows * d_in * 2);
+    l.total = l.partial = align(l.factor + (size_t)rows * 4);
+  }
+  const int slabs = (d_in + kSlabCols - 1) / kSlabCols;
+  const long long groups = (long long)((d_out + 16 * kTileTiles - 1) / (16 * kTileTiles)) * ((rows + kTileM - 1) / kTileM);
+  if (groups < kLinearGroups / 2) {
+    long long want = kLinearGroups / groups;
+    if (want > kMostSplits) want = kMostSplits;
+    if (want > slabs / 2) want = slabs / 2 > 1 ? slabs / 2 : 1;
+    const int per = (int)((slabs + want - 1) / want);
+    l.splits = (slabs + per - 1) / per;
+  }
+  if (l.splits > 1) l.total = align(l.partial + (size_t)l.splits * rows * d_out * 4);
+  return l;
+}
+hipError_t launch_linear_pack(const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
                               hipStream_t s);
 hipError_t launch_linear(int act, const LinearArgs& a, hipStream_t s);
 

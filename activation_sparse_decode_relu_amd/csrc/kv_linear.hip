@@ -2,24 +2,33 @@
 //
 // A code is u = q + 8.  Four bits put into the mantissa of 16.0 read 16 + u = 24 + q, in fp16 and in bf16, so two
 // codes of a word become two operands of a matrix instruction with one `and` and one `or` (the word is rotated by
-// four bits from pair to pair), and no conversion.  The 24 is taken off by the accumulator that the product
-// begins with, c = -24 sum x over the group, itself a product of the same x with a constant: all of it in fp32, off
-// by at most 2^-24 of 32 times the group's largest |x| a term.  Each group of 32 columns is one 16x16x32 product;
-// its sum, times the scale, is added in fp32.
-#include "kv_device.h"
+// four bits from pair to pair), and no conversion.
+//
+// Up to 64 rows are bound by reading the codes and x, and their sums are exact but for fp32's own rounding: the 24 is taken
+// off by the accumulator that a product begins with, c = -24 sum x over the group, itself a product of the same x
+// with a constant; each group of 32 columns is one 16x16x32 product, and its sum, times the scale, is added in fp32.
+//
+// More than 64 rows are bound by issue: on this hardware a vector ALU instruction runs beside a matrix instruction only in part
+// (a 16x16x32 one and n others take 15.6 + 3.7 n cycles together, a 32x32x16 one, twice the work, 19 + 3.9 n), and an
+// fp32 multiply-add for each output and group alone takes as many cycles as the product itself (2000 rows 4096 -> 12288:
+// 328 us).  So there code times scale is an fp16 operand, rounded to half a step of 2^-11, no more than an fp16 y itself
+// is, and the sums stay in 32x32x16 products.  bf16 rows are made fp16 for this, each by a power of two of its own, in the
+// caller's scratch: what is lost lies 2^-39 below a row's largest.
 #include "kv_linear.h"
+#include "kv_softmax.h"
 
 namespace pik {
 
 namespace {
 
+constexpr unsigned kTurn = 6;   // words are stored rotated left by as much, where fp16's operands have the first pair
 template <int ACT> struct Code;
 template <> struct Code<ACT_F16> {
-  static constexpr unsigned kTurn = 6, kMask = 0x03C003C0u, kOne = 0x4C004C00u;   // 16.0, steps of 2^-6
+  static constexpr unsigned kBack = 0, kMask = 0x03C003C0u, kOne = 0x4C004C00u;   // 16.0, steps of 2^-6
   static constexpr unsigned kMinus = 0xCE00CE00u;                                  // -24.0
 };
 template <> struct Code<ACT_BF16> {
-  static constexpr unsigned kTurn = 3, kMask = 0x00780078u, kOne = 0x41804180u;   // 16.0, steps of 2^-3
+  static constexpr unsigned kBack = 3, kMask = 0x00780078u, kOne = 0x41804180u;   // 16.0, steps of 2^-3
   static constexpr unsigned kMinus = 0xC1C0C1C0u;                                  // -24.0
 };
 
@@ -44,7 +53,7 @@ template <int ACT>
 __device__ __forceinline__ typename ActT<ACT>::V8 operand(unsigned w, unsigned one) {
   u32x4 r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = (__builtin_amdgcn_alignbit(w, w, 4 * j) & Code<ACT>::kMask) | one;
+  for (int j = 0; j < 4; ++j) r[j] = (__builtin_amdgcn_alignbit(w, w, 4 * j + Code<ACT>::kBack) & Code<ACT>::kMask) | one;
   return __builtin_bit_cast(typename ActT<ACT>::V8, r);
 }
 
@@ -67,7 +76,6 @@ __global__ __launch_bounds__(256) void k_linear_factor(const unsigned short* __r
 }
 
 // One wave a slab.
-template <int ACT>
 __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__ w, const unsigned short* __restrict__ scales,
                                                      uint8_t* __restrict__ packed, const float* __restrict__ factor, int d_in,
                                                      int d_out, int slabs, long long count) {
@@ -89,7 +97,7 @@ __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         r |= ((q >> (8 * i)) & 15u) << (4 * i) | ((q >> (8 * i + 4)) & 15u) << (16 + 4 * i);
-      out[j] = r << Code<ACT>::kTurn | r >> (32 - Code<ACT>::kTurn);
+      out[j] = r << kTurn | r >> (32 - kTurn);
     }
     *reinterpret_cast<u32x4*>(to + piece * 1024 + lane * 16) = out;
   }
@@ -107,7 +115,7 @@ __global__ __launch_bounds__(256) void k_linear_pack(const uint8_t* __restrict__
   *reinterpret_cast<unsigned*>(to + 2048 + lane * 4) = s;
 }
 
-// ---- one to 64 rows ------------------------------------------------------------------------------------
+// ---- up to 64 rows -------------------------------------------------------------------------------------
 
 // A slab of one tile as a wave holds it.
 struct Slab {
@@ -385,49 +393,91 @@ out:
   join_waves<ACT, NB, 4, T>(A, reinterpret_cast<float*>(s_mem), acc, tile0, 0, wave, waves);
 }
 
-// ---- more than 64 rows ---------------------------------------------------------------------------------
+// ---- more than 64 rows: fp16 operands --------------------------------------------------------------------------
 
-// Bound by issue: on this hardware a wave's vector ALU instruction runs beside a matrix instruction only in part (a
-// 16x16x32 one and n others take 15.6 + 3.7 n cycles together, a 32x32x16 one, twice the work, 19 + 3.9 n).  With an fp32
-// multiply-add for each output and group, as many cycles as the product itself, 2000 rows 4096 -> 12288 took 328 us.  So
-// with fp16 activations code times scale is an fp16 operand, rounded to half a step of 2^-11 (as much as y itself), and the
-// sums stay in the matrix instructions.  There is no packed arithmetic in bf16, whose operands stay whole numbers.
-// A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64.  x, codes and scales go to LDS
-// without passing registers: x in stages of 64 columns, one and a half ahead of the one in use, codes three.  Two buffers
-// and no more, so that three workgroups fit in a compute unit.
-constexpr int kTileM = 128, kTileN = 128;
-template <int ACT>
-__global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
-  using E = typename ActT<ACT>::T;
-  using V8 = typename ActT<ACT>::V8;
-  constexpr int kTiles = kTileN / 16, kRing = 2;
-  __shared__ __align__(16) char s_mem[kRing * kTileM * kStage * 2 + 2 * kTiles * 1024 + 2 * kTiles * 256];
-  XTile<V8>(*s_x)[kTileM / 16] = reinterpret_cast<XTile<V8>(*)[kTileM / 16]>(s_mem);
-  u32x4(*s_code)[kTiles][WAVE] = reinterpret_cast<u32x4(*)[kTiles][WAVE]>(s_mem + kRing * kTileM * kStage * 2);
-  u32x4(*s_scale)[kTiles][16] = reinterpret_cast<u32x4(*)[kTiles][16]>(s_mem + kRing * kTileM * kStage * 2 + 2 * kTiles * 1024);
-  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int across = (A.tiles + kTiles - 1) / kTiles;
-  const int row0 = (int)(blockIdx.x / across) * kTileM, tile0 = (int)(blockIdx.x % across) * kTiles;
-  const E* x0 = static_cast<const E*>(A.x) + (int64_t)row0 * A.x_stride;
-  unsigned xrow[4];   // this wave brings rows 32 wave .. of a stage; rows past the end are not stored
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Rows of bf16 as fp16, each times a power of two that brings its largest to [2^14, 2^15), and that power's inverse.
+__global__ __launch_bounds__(256) void k_linear_half(const bf16* __restrict__ x, int64_t stride, int d_in, f16* __restrict__ to,
+                                                     float* __restrict__ factor) {
+  __shared__ float s_top[4];
+  const int tid = threadIdx.x, row = blockIdx.x;
+  const bf16* from = x + (int64_t)row * stride;
+  float top = 0.0f;
+  for (int c = 8 * tid; c < d_in; c += 8 * 256) {
+    const float m = max8<ACT_BF16>(*reinterpret_cast<const bf16x8*>(from + c));
+    top = fmaxf(top, m);
+  }
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    xrow[e] = 2u * (unsigned)min(32 * wave + 8 * e + (lane >> 3), A.rows - 1 - row0) * (unsigned)A.x_stride;
+  for (int m = 1; m < WAVE; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
+  if (tid % WAVE == 0) s_top[tid / WAVE] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  float down;
+  const float up = query_scale(top, down);
+  for (int c = 8 * tid; c < d_in; c += 8 * 256)
+    *reinterpret_cast<f16x8*>(to + (size_t)row * d_in + c) =
+        query8<ACT_BF16>(*reinterpret_cast<const bf16x8*>(from + c), up);
+  if (tid == 0) factor[row] = down;
+}
+
+// Eight columns of a row of W as fp16 operands: code times scale.
+__device__ __forceinline__ f16x8 weights(unsigned word, f16 scale, unsigned one) {
+  const f16x8 raw = operand<ACT_F16>(word, one);
+  const f16x2 by = {scale, scale}, less = {(f16)24.0f, (f16)24.0f};
+  f16x8 w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const f16x2 y = (f16x2{raw[2 * e], raw[2 * e + 1]} - less) * by;   // the difference is exact
+    w[2 * e] = y.x;
+    w[2 * e + 1] = y.y;
+  }
+  return w;
+}
+
+// A 32x32x16 operand: row lane % 32, columns 8 (lane / 32) .. of the 16.  Operand m of group k of 32 rows in two tiles.
+__device__ __forceinline__ f16x8 x_operand32(const XTile<f16x8>* x, int k, int m) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  return x[(lane >> 4) & 1][lane & 15][(4 * k + 2 * m + (lane >> 5)) ^ (lane & 7)];
+}
+// Register e of a product is row 8 (e / 4) + 4 (lane / 32) + e % 4, column lane % 32.
+
+// A workgroup takes 128 rows and 128 outputs, four waves of 64 x 64, over one of `splits` ranges of slabs.  x, codes and
+// scales go to LDS without passing registers: x in stages of 64 columns, one and a half ahead of the one in use, codes
+// three.  Two buffers and no more, so that three workgroups fit in a compute unit (two took 256 us where this takes 232).
+template <int ACT>
+__global__ __launch_bounds__(256, 3) void k_linear_tile(const LinearArgs A) {
+  using E = typename ActT<ACT>::T;
+  constexpr int WN = 2, MT = 2, NT = 2, kM = kTileM, kTiles = kTileTiles, kRows = 4;   // kRows: eights of rows a wave brings
+  __shared__ __align__(16) char s_mem[2 * kM * kStage * 2 + 2 * kTiles * 1024 + 2 * kTiles * 256];
+  XTile<f16x8>(*s_x)[kM / 16] = reinterpret_cast<XTile<f16x8>(*)[kM / 16]>(s_mem);
+  u32x4(*s_code)[kTiles][WAVE] = reinterpret_cast<u32x4(*)[kTiles][WAVE]>(s_mem + 2 * kM * kStage * 2);
+  u32x4(*s_scale)[kTiles][16] = reinterpret_cast<u32x4(*)[kTiles][16]>(s_mem + 2 * kM * kStage * 2 + 2 * kTiles * 1024);
+  const int lane = threadIdx.x & (WAVE - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int wm = wave / WN, wn = wave % WN, c = lane & 31, part = lane >> 5;
+  const int across = (A.tiles + kTiles - 1) / kTiles;
+  const int tile0 = (int)(blockIdx.x % across) * kTiles, rest = (int)(blockIdx.x / across);
+  const int split = rest % A.splits, row0 = rest / A.splits * kM;
+  const int per = (A.slabs + A.splits - 1) / A.splits, first = split * per, end = min(first + per, A.slabs);
+  const f16* x0 = static_cast<const f16*>(A.x) + (int64_t)row0 * A.x_stride;
+  unsigned xrow[kRows];   // rows past the end are not stored
+#pragma unroll
+  for (int e = 0; e < kRows; ++e)
+    xrow[e] = 2u * (unsigned)min(8 * (kRows * wave + e) + (lane >> 3), A.rows - 1 - row0) * (unsigned)A.x_stride;
   const size_t tile_bytes = (size_t)A.slabs * kSlabBytes;
-  // and the codes of tiles 2 wave and 2 wave + 1
+  // this wave brings the codes of tiles 2 wave and 2 wave + 1
   const uint8_t* from[2];
 #pragma unroll
   for (int e = 0; e < 2; ++e) from[e] = A.packed + (size_t)min(tile0 + 2 * wave + e, A.tiles - 1) * tile_bytes;
-  const int stages = A.slabs * (kSlabCols / kStage);
   // past the end the last again, which nobody uses
   auto bring_x = [&](int stage, int slot) {
-    const unsigned at = stage_byte(min(stage, stages - 1) * kStage, A.d_in);
+    const unsigned at = stage_byte(min(stage, 4 * end - 1) * kStage, A.d_in);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) bring(x0, xrow[e] + at, &s_x[slot][2 * wave + e / 2][8 * (e % 2)][0]);
+    for (int e = 0; e < kRows; ++e)
+      bring(x0, xrow[e] + at, &s_x[slot][(kRows * wave + e) / 2][8 * ((kRows * wave + e) % 2)][0]);
   };
   auto bring_codes = [&](int piece, int slot) {   // of 128 columns
-    const int p = min(piece, 2 * A.slabs - 1);
+    const int p = min(piece, 2 * end - 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       bring(from[e] + (size_t)(p / 2) * kSlabBytes + 1024 * (p % 2), 16u * lane, &s_code[slot][2 * wave + e][0]);
@@ -435,81 +485,44 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
   const unsigned scale_at =   // four tiles a wave, and twice, so that every wave has asked for as many loads
       (unsigned)(min(tile0 + 4 * (wave & 1) + (lane >> 4), A.tiles - 1) - tile0) * (unsigned)tile_bytes + 2048u + 16u * (lane & 15);
   auto bring_scales = [&](int slab, int slot) {
-    bring(A.packed + (size_t)tile0 * tile_bytes + (size_t)min(slab, A.slabs - 1) * kSlabBytes, scale_at,
+    bring(A.packed + (size_t)tile0 * tile_bytes + (size_t)min(slab, end - 1) * kSlabBytes, scale_at,
           &s_scale[slot][4 * (wave & 1)][0]);
   };
-  // kFold: 2 x 2 tiles of 32 x 32, operands 2 t + m for columns 16 m .. of a group of tile t; else 4 x 4 of 16 x 16
-  constexpr bool kFold = ACT == ACT_F16;
-  const int c = kFold ? lane & 31 : lane & 15, part = kFold ? lane >> 5 : lane >> 4;   // this lane's row of x or W, and columns
-  typedef float f32x16 __attribute__((ext_vector_type(16)));
-  f32x16 sum[2][2];
-  float acc[4][4][4];
+  f32x16 acc[NT][MT];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < MT; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[j][b][i] = 0.0f;
-        sum[j / 2][b / 2][8 * (j % 2) + 4 * (b % 2) + i] = 0.0f;
-      }
-  const V8 minus = minus24<ACT>();
-  const unsigned one = sixteen<ACT>();
-  Late<4> late;
-  u32x2 code[2][4];      // of the stage at hand and the next one: a word for each of its two groups
-  f16x2 scale[2][4];     // and scale
-  V8 v[2][4];            // of the group at hand and the next one
-  auto read_x = [&](int slot, int k, V8 (&to)[4]) {
+      for (int e = 0; e < 16; ++e) acc[j][b][e] = 0.0f;
+  const unsigned one = sixteen<ACT_F16>();
+  // operands 2 t + m: columns 16 m .. of a group of tile t
+  u32x2 code[2][2 * NT];   // of the stage at hand and the next one: a word for each of its two groups
+  f16x2 scale[2][NT];      // and scale
+  f16x8 x[2][2 * MT];      // of the group at hand and the next one
+  auto read_x = [&](int slot, int k, f16x8 (&to)[2 * MT]) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int tile = kFold ? 4 * wm + 2 * (b / 2) + (c >> 4) : 4 * wm + b, chunk = kFold ? 2 * (b % 2) + part : part;
-      to[b] = s_x[slot][tile][c & 15][(4 * k + chunk) ^ (c & 7)];
+    for (int b = 0; b < 2 * MT; ++b) to[b] = x_operand32(&s_x[slot][2 * MT * wm + 2 * (b / 2)], k, b % 2);
+  };
+  auto read_codes = [&](int slab, int q, u32x2 (&to)[2 * NT], f16x2 (&scales)[NT]) {
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {
+      const int tile = 2 * (NT * wn + j / 2) + (c >> 4);
+      to[j] = *(reinterpret_cast<const u32x2*>(&s_code[q / 2][tile][16 * (2 * (j % 2) + part) + (c & 15)]) + q % 2);
+      if (j % 2 == 0) scales[j / 2] = *(reinterpret_cast<const f16x2*>(&s_scale[slab & 1][tile][c & 15]) + q);
     }
   };
-  auto read_codes = [&](int slab, int q, u32x2 (&to)[4], f16x2 (&scales)[4]) {
+  auto group = [&](const f16x8 (&v)[2 * MT], const u32x2 (&codes)[2 * NT], const f16x2 (&scales)[NT], int k) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int tile = kFold ? 4 * wn + 2 * (j / 2) + (c >> 4) : 4 * wn + j, chunk = kFold ? 2 * (j % 2) + part : part;
-      to[j] = *(reinterpret_cast<const u32x2*>(&s_code[q / 2][tile][16 * chunk + (c & 15)]) + q % 2);
-      if (!kFold || j % 2 == 0)
-        scales[j] = *(reinterpret_cast<const f16x2*>(&s_scale[slab & 1][tile][c & 15]) + q);
-    }
-  };
-  auto group = [&](const V8 (&x)[4], const u32x2 (&code)[4], const f16x2 (&scale)[4], int k) {
-    if constexpr (kFold) {
+    for (int j = 0; j < 2 * NT; ++j) {
+      const f16x8 w = weights(codes[j][k], scales[j / 2][k], one);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f16x2 by = {scale[j & ~1][k], scale[j & ~1][k]}, less = {(f16)24.0f, (f16)24.0f};
-        const V8 raw = operand<ACT>(code[j][k], one);
-        V8 w;
+      for (int b = 0; b < MT; ++b)
+        acc[j / 2][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v[2 * b + j % 2], w, acc[j / 2][b], 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const f16x2 y = (f16x2{raw[2 * e], raw[2 * e + 1]} - less) * by;   // the difference is exact
-          w[2 * e] = y.x;
-          w[2 * e + 1] = y.y;
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) sum[j / 2][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[2 * b + j % 2], w, sum[j / 2][b], 0, 0, 0);
+      for (int b = 0; b < MT; ++b) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
-      }
-    } else {
-      f32x4 c[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) c[b] = product<ACT>(x[b], minus, f32x4{0.f, 0.f, 0.f, 0.f});
-      late.add(acc[3]);
-      interleave<4>();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const V8 w = operand<ACT>(code[j][k], one);
-        f32x4 now[4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) now[b] = product<ACT>(x[b], w, c[b]);
-        if (j > 0) late.add(acc[j - 1]);
-        late.set(now, (float)scale[j][k]);
-        interleave<4>();
+        __builtin_amdgcn_sched_group_barrier(0x002, 16 / MT, 0);
       }
     }
   };
@@ -521,22 +534,22 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  bring_x(0, 0);
-  bring_codes(0, 0);
-  bring_scales(0, 0);
+  bring_x(4 * first, 0);
+  bring_codes(2 * first, 0);
+  bring_scales(first, first & 1);
   __builtin_amdgcn_sched_barrier(0);
-  bring_x(1, 1);
+  bring_x(4 * first + 1, 1);
   __builtin_amdgcn_sched_barrier(0);
-  bring_codes(1, 1);
-  meet(Count<6>{});
-  read_x(0, 0, v[0]);
-  read_codes(0, 0, code[0], scale[0]);
-  for (int slab = 0; slab < A.slabs; ++slab) {
+  bring_codes(2 * first + 1, 1);
+  meet(Count<kRows + 2>{});
+  read_x(0, 0, x[0]);
+  read_codes(first, 0, code[0], scale[0]);
+  for (int slab = first; slab < end; ++slab) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int stage = 4 * slab + q;
-      read_x(q % 2, 1, v[1]);
-      group(v[0], code[q % 2], scale[q % 2], 0);
+      read_x(q % 2, 1, x[1]);
+      group(x[0], code[q % 2], scale[q % 2], 0);
       // this stage has been read, and the next one is there, if not yet the codes that were asked for after it
       if (q == 0) meet(Count<2>{});
       else if (q == 2) meet(Count<3>{});
@@ -546,46 +559,64 @@ __global__ __launch_bounds__(256, 2) void k_linear_tile(const LinearArgs A) {
       if (q % 2 == 1) bring_codes(2 * slab + (q + 3) / 2, ((q + 3) / 2) % 2);
       if (q == 1) bring_scales(slab + 1, (slab + 1) & 1);
       __builtin_amdgcn_sched_barrier(0);
-      read_x((q + 1) % 2, 0, v[0]);
+      read_x((q + 1) % 2, 0, x[0]);
       read_codes(slab + (q + 1) / 4, (q + 1) % 4, code[(q + 1) % 2], scale[(q + 1) % 2]);
-      group(v[1], code[q % 2], scale[q % 2], 1);
+      group(x[1], code[q % 2], scale[q % 2], 1);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  if constexpr (!kFold) late.add(acc[3]);
   wait_loads<0>();   // nothing is on its way to LDS when the workgroup ends
-  // Four rows of an output: rows r .. r + 3 of this wave's 64.
-  const int left = A.rows - row0 - 64 * wm;
-  const E* add0 = static_cast<const E*>(A.add) + (int64_t)(row0 + 64 * wm) * A.add_stride;
-  E* y0 = static_cast<E*>(A.y) + (int64_t)(row0 + 64 * wm) * A.y_stride;
-  auto store4 = [&](int r, int n, float factor, float bias, const float (&sums)[4]) {
-    const E* add = add0 + (int64_t)r * A.add_stride + n;
-    E* y = y0 + (int64_t)r * A.y_stride + n;
+
+  // ---- out: this wave's rows from r0 on ------------------------------------------------------------------
+  const int r0 = row0 + 32 * MT * wm, left = A.rows - r0;
+  const E* add0 = static_cast<const E*>(A.add) + (int64_t)r0 * A.add_stride;
+  E* y0 = static_cast<E*>(A.y) + (int64_t)r0 * A.y_stride;
+  float* part0 = A.partial + ((size_t)split * A.rows + r0) * A.d_out;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (r + i >= left || n >= A.d_out) continue;
-      float v = fmaf(sums[i], factor, bias);
-      if (A.add != nullptr) v += (float)add[i * A.add_stride];
-      y[i * A.y_stride] = (E)v;
-    }
-  };
-  constexpr int kWide = kFold ? 32 : 16, kEach = 64 / kWide;
-#pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    const int n = (tile0 + 4 * wn) * 16 + j * kWide + c, at = min(n, A.d_out - 1);
+  for (int j = 0; j < NT; ++j) {
+    const int n = (tile0 + 2 * (NT * wn + j)) * 16 + c, at = min(n, A.d_out - 1);
     const float factor = A.factor[at], bias = A.bias != nullptr ? A.bias[at] : 0.0f;
 #pragma unroll
-    for (int b = 0; b < kEach; ++b) {
-      if constexpr (kFold) {
+    for (int b = 0; b < MT; ++b)
 #pragma unroll
-        for (int a = 0; a < 4; ++a)
-          store4(32 * b + 8 * a + 4 * part, n, factor, bias,
-                 {sum[j][b][4 * a], sum[j][b][4 * a + 1], sum[j][b][4 * a + 2], sum[j][b][4 * a + 3]});
-      } else {
-        store4(16 * b + 4 * part, n, factor, bias, {acc[j][b][0], acc[j][b][1], acc[j][b][2], acc[j][b][3]});
+      for (int a = 0; a < 4; ++a) {
+        const int r = 32 * b + 8 * a + 4 * part;
+        const E* add = add0 + (int64_t)r * A.add_stride + n;
+        E* y = y0 + (int64_t)r * A.y_stride + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (r + i >= left || n >= A.d_out) continue;
+          const float sum = acc[j][b][4 * a + i];
+          if (A.splits > 1) {
+            part0[(size_t)(r + i) * A.d_out + n] = sum;
+            continue;
+          }
+          float v = fmaf(sum, A.row_factor != nullptr ? factor * A.row_factor[r0 + r + i] : factor, bias);
+          if (A.add != nullptr) v += (float)add[i * A.add_stride];
+          y[i * A.y_stride] = (E)v;
+        }
       }
-    }
   }
+}
+
+// The ranges' sums, in their order, and out.
+template <int ACT>
+__global__ __launch_bounds__(256) void k_linear_join(const LinearArgs A) {
+  using E = typename ActT<ACT>::T;
+  const int blocks = (A.d_out + 255) / 256, t = (int)(blockIdx.x / blocks), n = (int)(blockIdx.x % blocks) * 256 + threadIdx.x;
+  if (n >= A.d_out) return;
+  const size_t step = (size_t)A.rows * A.d_out;
+  const float* from = A.partial + (size_t)t * A.d_out + n;
+  float v[kMostSplits], sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < kMostSplits; ++s) v[s] = from[min(s, A.splits - 1) * step];
+#pragma unroll
+  for (int s = 0; s < kMostSplits; ++s) sum += s < A.splits ? v[s] : 0.0f;
+  sum *= A.factor[n];
+  if (A.row_factor != nullptr) sum *= A.row_factor[t];
+  if (A.bias != nullptr) sum += A.bias[n];
+  if (A.add != nullptr) sum += (float)static_cast<const E*>(A.add)[(int64_t)t * A.add_stride + n];
+  static_cast<E*>(A.y)[(int64_t)t * A.y_stride + n] = (E)sum;
 }
 
 template <int ACT, int B>
@@ -609,16 +640,42 @@ hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
   if (a.rows <= kFewRows) return few_go<ACT, kFewRows>(a, s);
   if (a.rows <= 16) return rows_go<ACT, 1, 2, 8, 4, 2>(a, s);
   if (a.rows <= 32) return rows_go<ACT, 2, 2, 8, 2, 1>(a, s);
-  if (a.rows <= 64) return rows_go<ACT, 4, 3, 4, 2, 1>(a, s);
-  const long long grid = (long long)((a.tiles + kTileN / 16 - 1) / (kTileN / 16)) * ((a.rows + kTileM - 1) / kTileM);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_linear_tile<ACT>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  if (a.rows <= kExactRows) {
+    // the registers and LDS of eight waves fill a compute unit, and so the card is filled once: 64 rows 8192 -> 8192, 512
+    // tiles, 23.5 us by two tiles and eight waves, 24.7 by four waves, 31.5 by three tiles; 7168 -> 21504, 1344 tiles,
+    // 47.3 us by three tiles and four waves, 51.8 by two, 56.4 by two and eight waves
+    if (a.tiles <= 512) return rows_go<ACT, 4, 2, 8, 2, 1>(a, s);
+    return a.tiles <= 1024 ? rows_go<ACT, 4, 2, 4, 2, 1>(a, s) : rows_go<ACT, 4, 3, 4, 2, 1>(a, s);
+  }
+  LinearArgs b = a;
+  const LinearScratch layout = linear_scratch(ACT, a.rows, a.d_in, a.d_out);
+  char* scratch = static_cast<char*>(a.scratch);
+  b.splits = layout.splits;
+  b.partial = reinterpret_cast<float*>(scratch + layout.partial);
+  if constexpr (ACT == ACT_BF16) {
+    f16* x = reinterpret_cast<f16*>(scratch + layout.x);
+    float* factor = reinterpret_cast<float*>(scratch + layout.factor);
+    hipLaunchKernelGGL(k_linear_half, dim3((unsigned)a.rows), dim3(256), 0, s, static_cast<const bf16*>(a.x), a.x_stride, a.d_in,
+                       x, factor);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    b.x = x;
+    b.x_stride = a.d_in;
+    b.row_factor = factor;
+  }
+  const long long grid = (long long)((a.tiles + kTileTiles - 1) / kTileTiles) * b.splits * ((a.rows + kTileM - 1) / kTileM);
+  const long long join = (long long)((a.d_out + 255) / 256) * a.rows;
+  if (grid > 0x7fffffff || (b.splits > 1 && join > 0x7fffffff)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_linear_tile<ACT>), dim3((unsigned)grid), dim3(256), 0, s, b);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || b.splits == 1) return e;
+  hipLaunchKernelGGL((k_linear_join<ACT>), dim3((unsigned)join), dim3(256), 0, s, b);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
+hipError_t launch_linear_pack(const void* w, const void* scales, void* packed, float* factor, int d_in, int d_out,
                               hipStream_t s) {
   const int slabs = (d_in + kSlabCols - 1) / kSlabCols, tiles = (d_out + kSlabRows - 1) / kSlabRows;
   const long long count = (long long)tiles * slabs, grid = (count + 3) / 4;
@@ -630,12 +687,8 @@ hipError_t launch_linear_pack(int act, const void* w, const void* scales, void* 
                      d_out, tiles * kSlabRows);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (act == ACT_F16)
-    hipLaunchKernelGGL((k_linear_pack<ACT_F16>), dim3((unsigned)grid), dim3(256), 0, s, codes, halves, to, factor, d_in, d_out,
-                       slabs, count);
-  else
-    hipLaunchKernelGGL((k_linear_pack<ACT_BF16>), dim3((unsigned)grid), dim3(256), 0, s, codes, halves, to, factor, d_in, d_out,
-                       slabs, count);
+  hipLaunchKernelGGL(k_linear_pack, dim3((unsigned)grid), dim3(256), 0, s, codes, halves, to, factor, d_in, d_out, slabs,
+                     count);
   return hipGetLastError();
 }
 

@@ -70,7 +70,7 @@ pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void
     return fail(PI_ERR_WORKSPACE, "packed must be %zu bytes, %zu-byte aligned", need, (size_t)kAlign);
   pi_linear* h = new (std::nothrow) pi_linear{*desc, static_cast<const uint8_t*>(packed), bias};
   if (h == nullptr) return fail(PI_ERR_INVALID, "out of host memory");
-  const hipError_t e = pik::launch_linear_pack(desc->act_dtype, w, scales, packed, const_cast<float*>(h->factor()), desc->d_in,
+  const hipError_t e = pik::launch_linear_pack(w, scales, packed, const_cast<float*>(h->factor()), desc->d_in,
                                                desc->d_out, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) {
     delete h;
@@ -83,6 +83,14 @@ pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void
 pi_status pi_linear_destroy(pi_linear* h) {
   if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
   delete h;
+  return ok();
+}
+
+pi_status pi_linear_scratch_bytes(const pi_linear* h, int32_t rows, size_t* bytes) {
+  if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
+  if (bytes == nullptr) return fail(PI_ERR_INVALID, "bytes is NULL");
+  if (rows < 0 || rows > kMaxRows) return fail(PI_ERR_INVALID, "rows=%d must lie in [0, %d]", rows, kMaxRows);
+  *bytes = pik::linear_scratch(h->desc.act_dtype, rows, h->desc.d_in, h->desc.d_out).total;
   return ok();
 }
 
@@ -101,7 +109,11 @@ pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stre
     return fail(PI_ERR_INVALID, "add_stride=%lld must not be negative", (long long)args->add_stride);
   if (args->rows > 1 && args->y_stride < d.d_out)
     return fail(PI_ERR_INVALID, "y_stride=%lld is less than d_out=%d", (long long)args->y_stride, d.d_out);
+  const size_t need = pik::linear_scratch(d.act_dtype, args->rows, d.d_in, d.d_out).total;
+  if (need > 0 && (args->scratch == nullptr || !aligned(args->scratch, 16) || args->scratch_bytes < need))
+    return fail(PI_ERR_WORKSPACE, "scratch must be %zu bytes, 16-byte aligned", need);
   pik::LinearArgs a{};
+  a.scratch = args->scratch;
   a.packed = h->packed;
   a.factor = h->factor();
   a.bias = h->bias;

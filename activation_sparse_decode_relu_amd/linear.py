@@ -19,7 +19,7 @@ LINEAR_ACTS = {"f16": PI_LINEAR_F16, "bf16": PI_LINEAR_BF16}
 _ACT_TORCH = {PI_LINEAR_F16: torch.float16, PI_LINEAR_BF16: torch.bfloat16}
 
 LINEAR_EXPORTED = ("pi_linear_abi_version", "pi_linear_packed_bytes", "pi_linear_create", "pi_linear_destroy",
-                   "pi_linear_forward")
+                   "pi_linear_scratch_bytes", "pi_linear_forward")
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -30,7 +30,7 @@ class LinearDesc(ctypes.Structure):
 
 class LinearArgs(ctypes.Structure):
     _fields_ = [("x", _vp), ("add", _vp), ("y", _vp), ("x_stride", _i64), ("add_stride", _i64), ("y_stride", _i64),
-                ("rows", _i32)]
+                ("scratch", _vp), ("scratch_bytes", ctypes.c_size_t), ("rows", _i32)]
 
 
 def _declare() -> None:
@@ -38,6 +38,7 @@ def _declare() -> None:
     sigs = dict(pi_linear_packed_bytes=[p(LinearDesc), p(ctypes.c_size_t)],
                 pi_linear_create=[p(LinearDesc), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, p(_vp)],
                 pi_linear_destroy=[_vp],
+                pi_linear_scratch_bytes=[_vp, _i32, p(ctypes.c_size_t)],
                 pi_linear_forward=[_vp, p(LinearArgs), _vp])
     for name, args in sigs.items():
         fn = getattr(LIB, name)
@@ -75,8 +76,8 @@ class Linear:
         scales   fp16 [d_out][d_in / 32]     one for 32 consecutive elements of a row
         bias     fp32 [d_out], or None
 
-    The weights are laid out once, here (`packed`, made unless given); w and scales may then be let go of.  Calls have
-    no workspace and may run at the same time on several streams.
+    The weights are laid out once, here (`packed`, made unless given); w and scales may then be let go of.  Calls may
+    run at the same time on several streams.
     """
 
     def __init__(self, w, scales, act_dtype="f16", bias=None, packed=None, stream=None):
@@ -172,12 +173,24 @@ class Linear:
             with torch.cuda.device(self.device.index):
                 check(fn(*args))
 
-    def forward(self, x, y, add=None, stream=None) -> None:
-        """y [rows][d_out] = x [rows][d_in] W^T + bias + add [rows][d_out].  Rows may be strided (x's by a multiple of
-        8 elements), the innermost dimension is contiguous.  y may be add itself."""
+    def scratch_bytes(self, rows) -> int:
+        """Bytes of scratch that forward takes for `rows` rows."""
+        if rows >> 31:
+            raise _invalid(f"rows={rows} does not fit in 32 bits")
+        out = ctypes.c_size_t(0)
+        check(LIB.pi_linear_scratch_bytes(self._live(), rows, _byref(out)))
+        return int(out.value)
+
+    def _live(self):
         if self.handle is None:
             raise _invalid("the weights are closed")
-        d = self.desc
+        return self.handle
+
+    def forward(self, x, y, add=None, scratch=None, stream=None) -> None:
+        """y [rows][d_out] = x [rows][d_in] W^T + bias + add [rows][d_out].  Rows may be strided (x's by a multiple of
+        8 elements), the innermost dimension is contiguous.  y may be add itself.  scratch: scratch_bytes(rows) bytes
+        (0 up to 64 rows), made here unless given."""
+        d, handle = self.desc, self._live()
         xs = self._rows(x, "x", d.d_in)
         rows = x.shape[0]
         ys = self._rows(y, "y", d.d_out, rows)
@@ -186,5 +199,18 @@ class Linear:
         adds = 0 if add is None else self._rows(add, "add", d.d_out, rows)
         if rows >> 31:
             raise _invalid(f"rows={rows} does not fit in 32 bits")
-        args = LinearArgs(x.data_ptr(), None if add is None else add.data_ptr(), y.data_ptr(), xs, adds, ys, rows)
-        self._run(LIB.pi_linear_forward, self.handle, _byref(args), self._stream(stream, (x, y, add)))
+        need = self.scratch_bytes(rows) if scratch is None and rows > 64 else 0
+        if need:
+            if stream is None:
+                scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+            else:   # of the stream that uses it
+                with torch.cuda.stream(stream):
+                    scratch = torch.empty(need, dtype=torch.uint8, device=self.device)
+        size = 0
+        if scratch is not None:
+            if not isinstance(scratch, torch.Tensor) or scratch.device != self.device or not scratch.is_contiguous():
+                raise _invalid(f"scratch must be a contiguous tensor on {self.device}")
+            size = scratch.numel() * scratch.element_size()
+        args = LinearArgs(x.data_ptr(), None if add is None else add.data_ptr(), y.data_ptr(), xs, adds, ys,
+                          None if scratch is None else scratch.data_ptr(), size, rows)
+        self._run(LIB.pi_linear_forward, handle, _byref(args), self._stream(stream, (x, y, add, scratch)))

@@ -13,18 +13,20 @@
  * [ceil(d_out / 16)][ceil(d_in / 256)] slabs of 2304 bytes: two KB of codes, one for each 128 columns, and fp16
  * scales [16 rows][8 groups].  Word j of the 16 bytes 16 l .. of a KB holds the columns 32 j + 8 (l / 16) .. + 8
  * of row l % 16, as u = q + 8: column 2 i at bit 4 i and column 2 i + 1 at bit 16 + 4 i, the word rotated left
- * by 6 bits (fp16 activations) or 3 (bf16).  Rows and columns that are not there have q = 0 and scale 0.  Behind the
+ * by 6 bits.  Rows and columns that are not there have q = 0 and scale 0.  Behind the
  * slabs stands a power of two for each row (fp32) that its scales were divided by, which brings the largest of them to
  * [8, 16); what a scale 2^-17 of that and less loses lies under the sums' own rounding.
  *
  * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
  * --------------------------------------------------------------------------------------------------
  * - Ownership: the caller allocates all device memory; a handle borrows it until pi_linear_destroy.
- * - Streams: calls only enqueue on `stream`.  A handle has no workspace: its calls may run at the same time.
- * - Products of whole numbers and activations are summed in fp32 by groups of 32, and the groups' sums, times
- *   their scales, in fp32; y is rounded once.  With fp16 activations and more than 64 rows, code times scale is
- *   rounded to fp16 (half a step of 2^-11) and summed in fp32.  A row's result depends on its own x, and, in its last
- *   bits, on the number of rows of the call; it does not depend on the order in which workgroups run.
+ * - Streams: calls only enqueue on `stream`.  A handle has no workspace: its calls may run at the same time, each
+ *   with a scratch of its own.
+ * - Up to 64 rows: products of whole numbers and activations are summed in fp32 by groups of 32, and the groups'
+ *   sums, times their scales, in fp32.  More rows: code times scale is rounded to fp16 (half a step of 2^-11), and
+ *   so are bf16 rows, relative to their largest (exact down to 2^-29 of it, and 2^-39 of it lost at most); products
+ *   are summed in fp32.  y is rounded once.  A row's result depends on its own x, and, in its last bits, on the number
+ *   of rows of the call; it does not depend on the order in which workgroups run.
  * - A row of x that holds an infinity, a NaN, or (bf16) a magnitude of 2^118 and more may come out as NaN, other
  *   rows are not touched by it.
  */
@@ -55,6 +57,8 @@ typedef struct pi_linear_args {
   int64_t x_stride;   /* from row to row, in elements: a multiple of 8 up to 2^23 (looked at for several rows) */
   int64_t add_stride; /* in elements                                                        */
   int64_t y_stride;   /* in elements, at least d_out                                        */
+  void* scratch;      /* pi_linear_scratch_bytes, 16-byte aligned; not looked at where that is 0 */
+  size_t scratch_bytes;
   int32_t rows;       /* 0 to 2^24; 0 enqueues nothing                                      */
 } pi_linear_args;
 
@@ -75,6 +79,9 @@ pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void
 
 /* Release the handle (host memory only). */
 pi_status pi_linear_destroy(pi_linear* h);
+
+/* Bytes of scratch a call with as many rows takes: 0 up to 64 rows.  Host only. */
+pi_status pi_linear_scratch_bytes(const pi_linear* h, int32_t rows, size_t* bytes);
 
 /* y = W x + bias + add for every row. */
 pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stream);

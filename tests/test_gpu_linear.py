@@ -3,9 +3,10 @@
 Bounds.  A group's sum is a product of whole numbers 24 + q with x, begun with -24 sum x, itself summed in fp32: 32 terms
 of at most 24 |x| and 33 of at most 55 of the group's sum |x| (the beginning among them), each addition off by 2^-24:
 (32 * 24 + 33 * 55) 2^-24 < 2600 * 2^-24 of it, times the scale.  The G groups, the waves, bias and add join in fp32:
-(G + 12) 2^-24 of the terms' magnitudes.  y is rounded once: half a step of its type.  With fp16 and more than 64 rows a
+(G + 12) 2^-24 of the terms' magnitudes.  y is rounded once: half a step of its type.  With more than 64 rows a
 weight is rounded to fp16, relative to the row's largest scale in [8, 16): half a step, 2^-11 of it, or 2^-25 / 8 of that
-scale where that is more; and scales of less than 2^-17 of the largest lose as little, times 8.
+scale where that is more; scales of less than 2^-17 of the largest lose as little, times 8; and bf16 rows of x are fp16
+relative to their largest in [2^14, 2^15): exact, or off by 2^-25 / 2^14 of it.
 """
 
 import numpy as np
@@ -58,8 +59,9 @@ class Rig:
         tol = (2600 * 2.0 ** -24 * (np.abs(x) @ self.s.T) + (self.d_in // 32 + 12) * 2.0 ** -24 * mass +
                EPS[self.act] * np.abs(ref) + TINY[self.act])
         tol += 2.0 ** -25 * (np.abs(x).sum(1, keepdims=True) * self.s.max(1))          # scales kept relative to the row's largest
-        if self.act == "f16" and x.shape[0] > 64:
+        if x.shape[0] > 64:
             tol += 2.0 ** -11 * (np.abs(x) @ np.abs(self.w).T) * (1 + EPS[self.act])
+            tol += 2.0 ** -39 * np.abs(x).max(1, keepdims=True) * np.abs(self.w).sum(1)
         err = np.abs(y.double().cpu().numpy() - ref)
         assert np.all(err <= tol), f"off by {np.max(err / tol):.2f} times its bound"
 
@@ -84,6 +86,15 @@ def test_rows(rows, act):
 def test_widths(d_in, rows):
     announce(f"linear d_in {d_in}, rows {rows}")
     Rig(d_in, 100, "f16", seed=d_in).run(rows)
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("d_in, d_out", [(512, 200), (768, 100), (1312, 333), (4096, 129), (11008, 1000)])
+@pytest.mark.parametrize("rows", [65, 127, 128, 129, 400])
+def test_split_columns(rows, d_in, d_out, act):
+    """Few workgroups: the columns in ranges whose sums are joined."""
+    announce(f"linear split {rows} {d_in} {d_out} {act}")
+    Rig(d_in, d_out, act, bias=True, seed=rows).run(rows, add=True)
 
 
 @pytest.mark.parametrize("d_out", [1, 2, 15, 16, 17, 31, 33, 63, 65, 127, 129, 1000, 5001])
@@ -162,6 +173,57 @@ def test_extreme_inputs(act, value):
     y = torch.empty(3, 16, dtype=DT[act], device="cuda")
     m.forward(x.cuda(), y)
     assert torch.equal(y.cpu(), ref.to(DT[act]))
+
+
+def test_scratch_of_the_callers():
+    announce("linear scratch")
+    import activation_sparse_decode_relu_amd as pi
+    r = Rig(320, 40, "bf16", seed=12)
+    x = r.x(70).cuda()
+    y, z = (torch.empty(70, 40, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    r.m.forward(x, y)
+    need = r.m.scratch_bytes(70)
+    scratch = torch.full((need + 16,), 77, dtype=torch.uint8, device="cuda")
+    r.m.forward(x, z, scratch=scratch)
+    assert torch.equal(y, z) and bool((scratch[need:] == 77).all())
+    with pytest.raises(pi.PiError) as e:
+        r.m.forward(x, z, scratch=scratch[:need - 1])
+    assert e.value.status == 2
+
+
+@pytest.mark.parametrize("rows", [20, 50, 100, 260])
+def test_rows_of_very_different_size(rows):
+    """bf16 rows from 2^-100 to 2^100, zero rows among them: each is as accurate as alone."""
+    announce(f"linear row sizes {rows}")
+    r = Rig(512, 33, "bf16", seed=rows)
+    x = r.x(rows)
+    x *= torch.exp2(torch.from_numpy(r.rng.integers(-100, 100, (rows, 1)).astype(np.float32))).bfloat16()
+    x[3] = 0
+    y = torch.empty(rows, 33, dtype=torch.bfloat16, device="cuda")
+    r.m.forward(x.cuda(), y)
+    r.check(x, y)
+
+
+def test_scales_of_very_different_size():
+    """Rows of W from fp16's smallest scales to its largest."""
+    announce("linear scale sizes")
+    import activation_sparse_decode_relu_amd as pi
+    rng = np.random.default_rng(8)
+    q = rng.integers(-8, 8, (48, 256))
+    scales = np.exp2(rng.integers(-24, 16, (48, 1)) + np.zeros((1, 8))).astype(np.float16)
+    scales[5], scales[6, 3] = 0, 65504
+    codes = pack_nibbles(q)
+    m = pi.Linear(torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda(), act_dtype="bf16")
+    w = oracle.dequant_q4g32(codes, scales)
+    for rows in (1, 10, 30, 60, 100):
+        x = torch.from_numpy(rng.integers(-3, 4, (rows, 256)).astype(np.float64)).bfloat16()
+        y = torch.empty(rows, 48, dtype=torch.bfloat16, device="cuda")
+        m.forward(x.cuda(), y)
+        ref = x.double().numpy() @ w.T
+        keep = [i for i in range(48) if i != 6]     # exact sums; row 6 mixes 65504 with smaller ones
+        assert torch.equal(y.cpu()[:, keep], torch.from_numpy(ref).bfloat16()[:, keep]), f"{rows} rows"
+        mass = np.abs(x.double().numpy()) @ np.abs(w).T
+        assert np.all(np.abs(y.cpu().double().numpy() - ref)[:, 6] <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * mass[:, 6])
 
 
 def test_no_rows():

@@ -37,7 +37,7 @@ def test_header_is_plain_c(tmp_path):
 
 def test_struct_layouts():
     assert ctypes.sizeof(lin.LinearDesc) == 12
-    assert ctypes.sizeof(lin.LinearArgs) == 56
+    assert ctypes.sizeof(lin.LinearArgs) == 72
 
 
 @pytest.mark.parametrize("d_in, d_out, tiles, slabs", [(32, 1, 1, 1), (256, 16, 1, 1), (288, 17, 2, 2), (8192, 10240, 640, 32)])
@@ -81,13 +81,13 @@ def test_null_handles():
 class _Handle:
     """A handle as the library lays it out, for refusals that come before anything is enqueued: desc, packed, bias."""
 
-    def __init__(self, d_in, d_out):
+    def __init__(self, d_in, d_out, act="f16"):
         class Raw(ctypes.Structure):
             _fields_ = [("desc", lin.LinearDesc), ("packed", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
-        self.raw = Raw(pi.linear_desc(d_in, d_out), FAKE, None)
+        self.raw = Raw(pi.linear_desc(d_in, d_out, act), FAKE, None)
 
     def forward(self, **change):
-        a = {**dict(x=FAKE, add=None, y=FAKE, x_stride=64, add_stride=0, y_stride=8, rows=2), **change}
+        a = {**dict(x=FAKE, add=None, y=FAKE, x_stride=64, add_stride=0, y_stride=8, scratch=None, scratch_bytes=0, rows=2), **change}
         return pi.LIB.pi_linear_forward(ctypes.byref(self.raw), ctypes.byref(lin.LinearArgs(**a)), None)
 
 
@@ -96,6 +96,25 @@ class _Handle:
                                     dict(add=FAKE, add_stride=-8), dict(y_stride=7)])
 def test_forward_refusals(change):
     assert _Handle(64, 8).forward(**change) == 1 and pi.last_error()
+
+
+def test_scratch():
+    """fp16 rows and factors (bf16), and a sum for each range of columns where few workgroups would be busy."""
+    def need(d_in, d_out, rows, act):
+        out = ctypes.c_size_t(9)
+        assert pi.LIB.pi_linear_scratch_bytes(ctypes.byref(_Handle(d_in, d_out, act).raw), rows, ctypes.byref(out)) == 0
+        return out.value
+    assert [need(8192, 8192, rows, "bf16") for rows in (0, 1, 64)] == [0, 0, 0]
+    assert need(64, 8, 65, "f16") == 0 and need(64, 8, 65, "bf16") == 8448 + 512    # one slab: one range
+    assert need(4096, 12288, 2000, "f16") == 0                                   # workgroups enough
+    assert need(8192, 8192, 128, "f16") == 8 * 128 * 8192 * 4                    # 64 of them, 32 slabs in 8 ranges
+    assert need(7168, 21504, 100, "bf16") == 100 * 7168 * 2 + 512 + 3 * 100 * 21504 * 4
+    h, out, size = _Handle(64, 8, "bf16"), ctypes.c_size_t(9), 8448 + 512
+    for bad in (dict(scratch=None), dict(scratch=FAKE + 8), dict(scratch_bytes=size - 1)):
+        assert h.forward(rows=65, **{**dict(scratch=FAKE, scratch_bytes=size), **bad}) == 2
+    assert pi.LIB.pi_linear_scratch_bytes(None, 1, ctypes.byref(out)) == 1
+    assert pi.LIB.pi_linear_scratch_bytes(ctypes.byref(h.raw), -1, ctypes.byref(out)) == 1
+    assert pi.LIB.pi_linear_scratch_bytes(ctypes.byref(h.raw), 1, None) == 1
 
 
 def test_no_rows_enqueue_nothing():
