@@ -58,9 +58,16 @@ enum : int { ATTEND_ALL = 0, ATTEND_SHARED = 1, ATTEND_OWN = 2 };
 struct KvSharedArgs : KvAttendArgs {
   const int* groups;   // [n_groups + 1]: group g is the sequences groups[g] .. groups[g + 1] of the call
   const int* plan;     // [n_groups + n]: shared tokens of each group, and of each sequence's group
-  float* state;        // [rows][heads][D + 4]: O' and rr, mm, l (kv_softmax.h)
+  float* state;        // [parts][rows][heads][D + 4]: O' and rr, mm, l (kv_softmax.h)
   int n_groups;
+  int parts;           // into how many parts a group's tokens are split at most (kernel of many rows), 1 for few rows
 };
+// Workgroups that the shared tokens are split for where there are many rows, and the parts that this makes.
+constexpr int kSharedParts = 512;
+constexpr int shared_parts(long long rows, int group, int kv_heads, int n_groups) {
+  const long long items = (rows * group / 128 + n_groups) * kv_heads;
+  return items > kSharedParts / 2 ? 1 : (int)(kSharedParts / items);
+}
 struct KvShareArgs {
   KvView c;
   const int* groups;
@@ -68,12 +75,16 @@ struct KvShareArgs {
   int n_groups;
 };
 hipError_t launch_kv_share(const KvShareArgs& a, hipStream_t s);
+// Joins the parts of all states; `parts` is 1 from then on.
+hipError_t launch_kv_state_join(const KvSharedArgs& a, hipStream_t s);
 hipError_t launch_kv_step_shared(int act, int code, int mode, const KvSharedArgs& a, hipStream_t s);
 hipError_t launch_kv_tile_shared(int act, int code, int mode, const KvSharedArgs& a, hipStream_t s);
 
 // Few rows of a cached head (max_new * group up to kStepRows): items (sequences times cached heads) in pieces, one
 // workgroup each, see kv_step.hip.  S is at least kStepGrain blocks.
-constexpr int kStepRows = 64, kStepGrain = 8;
+// (Behind shared tokens items are short, and a part to join costs more than some 24 blocks: 64 sequences of 30 to 800 own tokens,
+// 8 heads, 108 us for two layers with 32, 123 with 8.)
+constexpr int kStepRows = 64, kStepGrain = 8, kOwnGrain = 32;
 // tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.  Eight
 // waves instead of four where 33 to 64 rows have 64 dims: half as many parts to join (four tokens over 100003, 16
 // query heads to a cached one: 46.0 against 50.5 us); with 128 dims LDS does not hold eight waves' parts.

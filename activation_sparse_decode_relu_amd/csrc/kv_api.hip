@@ -230,8 +230,9 @@ pi_status check_groups(const pi_kv_batch* b, const int32_t* groups, int32_t n_gr
   return check_ints(groups, "groups");
 }
 
+// A state for each row and head, and for each part in which a group's shared tokens may be taken.
 size_t state_bytes(const pi_kv_desc& d, int32_t rows) {
-  return (size_t)rows * d.heads * (d.head_dim + 4) * sizeof(float);
+  return (size_t)pik::shared_parts(rows, d.heads / d.kv_heads, d.kv_heads, 1) * rows * d.heads * (d.head_dim + 4) * sizeof(float);
 }
 
 void fill_attend(pik::KvAttendArgs& a, const pi_kv* h, int32_t layer, const pi_kv_attend_args* args,
@@ -394,14 +395,22 @@ pi_status pi_kv_attend_shared(pi_kv* h, int32_t layer, const pi_kv_attend_args* 
   a.state = static_cast<float*>(shared->state);
   a.n_groups = shared->n_groups;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  for (int mode : {pik::ATTEND_SHARED, pik::ATTEND_OWN}) {
-    a.max_new = mode == pik::ATTEND_SHARED ? shared->max_rows : args->max_new;
-    const bool few = few_rows(a, a.max_new, mode == pik::ATTEND_SHARED ? a.n_groups : a.c.n);
-    const hipError_t e = few ? pik::launch_kv_step_shared(h->desc.act_dtype, h->desc.code, mode, a, s)
-                             : pik::launch_kv_tile_shared(h->desc.act_dtype, h->desc.code, mode, a, s);
-    if (e != hipSuccess) return launched(e, "attend_shared");
+  const int act = h->desc.act_dtype, code = h->desc.code;
+  const int own = a.max_new;
+  a.max_new = shared->max_rows;
+  const bool few = few_rows(a, a.max_new, a.n_groups);
+  a.parts = few ? 1 : pik::shared_parts(batch->rows, a.group, a.c.kv_heads, a.n_groups);
+  hipError_t e = few ? pik::launch_kv_step_shared(act, code, pik::ATTEND_SHARED, a, s)
+                     : pik::launch_kv_tile_shared(act, code, pik::ATTEND_SHARED, a, s);
+  if (e != hipSuccess) return launched(e, "attend_shared");
+  a.max_new = own;
+  if (a.parts > 1 && (int64_t)own * a.group > 32) {
+    if ((e = pik::launch_kv_state_join(a, s)) != hipSuccess) return launched(e, "attend_shared");
+    a.parts = 1;
   }
-  return ok();
+  e = few_rows(a, a.max_new, a.c.n) ? pik::launch_kv_step_shared(act, code, pik::ATTEND_OWN, a, s)
+                                    : pik::launch_kv_tile_shared(act, code, pik::ATTEND_OWN, a, s);
+  return launched(e, "attend_shared");
 }
 
 pi_status pi_rope_create(const pi_rope_desc* desc, pi_rope** out) {

@@ -87,26 +87,53 @@ __device__ __forceinline__ int item_owner(const AttendArgs<MODE>& A, int slot, i
 
 // ---- the states of shared tokens ----------------------------------------------------------------------
 
+// The kernel of many rows splits the 64-token tiles of a group: into how many parts, and of how many tiles.
+constexpr int kMinTiles = 4;    // tiles a part is worth at least
+__device__ __forceinline__ int tiles_each(int tiles, int splits) { return max((tiles + splits - 1) / splits, kMinTiles); }
+__device__ __forceinline__ int parts_of(const KvSharedArgs& A, int shared) {
+  if (A.parts == 1) return 1;
+  const int tiles = (shared / kKvBlock + 1) / 2, per = tiles_each(tiles, A.parts);
+  return (tiles + per - 1) / per;
+}
+
 template <int D>
-__device__ __forceinline__ float* state_at(const KvSharedArgs& A, int row, int head) {
-  return A.state + ((size_t)row * A.heads + head) * (D + 4);
+__device__ __forceinline__ float* state_at(const KvSharedArgs& A, int part, int row, int head) {
+  return A.state + (((size_t)part * A.c.rows + row) * A.heads + head) * (D + 4);
 }
 // Four dims of a row's O', and with the first its state.
 template <int D>
-__device__ __forceinline__ void put_state(const KvSharedArgs& A, int row, int head, int d, const f32x4& v, const RowState& a) {
-  float* to = state_at<D>(A, row, head);
+__device__ __forceinline__ void put_state(const KvSharedArgs& A, int part, int row, int head, int d, const f32x4& v,
+                                          const RowState& a) {
+  float* to = state_at<D>(A, part, row, head);
   *reinterpret_cast<f32x4*>(to + d) = v;
   if (d == 0) *reinterpret_cast<f32x4*>(to + D) = f32x4{a.rr, a.mm, a.l, 0.f};
 }
-// Four dims of a row's O' and its state, joined with what put_state left.
+// Four dims of a row's O' and its state, joined with what put_state left in `parts` parts, in their order.
 template <int D>
-__device__ __forceinline__ void join_state(const KvSharedArgs& A, int row, int head, int d, f32x4& v, RowState& a) {
-  const float* from = state_at<D>(A, row, head);
-  const f32x4 u = *reinterpret_cast<const f32x4*>(from + d), s = *reinterpret_cast<const f32x4*>(from + D);
-  RowState b{s.x, s.y, s.z};
+__device__ __forceinline__ void join_state(const KvSharedArgs& A, int parts, int row, int head, int d, f32x4& v, RowState& a) {
+  constexpr int kBatch = 4;   // parts whose loads are on their way together
+  const float* from = state_at<D>(A, 0, row, head);
+  const size_t step = (size_t)A.c.rows * A.heads * (D + 4);
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  RowState b{-INFINITY, -INFINITY, 0.0f};
   float fb, fa;
+  for (int p0 = 0; p0 < parts; p0 += kBatch) {
+    f32x4 u[kBatch], s[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const float* at = from + min(p0 + e, parts - 1) * step;
+      u[e] = *reinterpret_cast<const f32x4*>(at + d);
+      s[e] = *reinterpret_cast<const f32x4*>(at + D);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e)
+      if (p0 + e < parts) {
+        join(b, RowState{s[e].x, s[e].y, s[e].z}, fb, fa);
+        sum = sum * fb + u[e] * fa;
+      }
+  }
   join(b, a, fb, fa);
-  v = u * fb + v * fa;
+  v = sum * fb + v * fa;
   a = b;
 }
 

@@ -3,8 +3,11 @@
 //
 // Two launches of the kernels of kv_step.h and kv_tile.h, each by its own number of rows.  The first takes groups as
 // items, all of a group's rows over its shared blocks, with no mask since every row stands behind them, and leaves each
-// row's O' and state (fp32) in the caller's scratch.  The second takes the sequences from their first own block
-// on, and joins that with the states where it would store its rows.
+// row's O' and state (fp32) in the caller's scratch, in several parts where many rows' tokens are split.  The second takes
+// the sequences from their first own block on, and joins that with the states where it would store its rows.  Parts are
+// joined there too while it has up to 32 rows of a cached head (two layers of 64 sequences on 4096 shared tokens: 108 us,
+// 116 with a launch between the two); where it has more, a lane's rows lie far apart, and a launch of its own joins them
+// (two layers of 8 sequences, 80 rows of a head, on 20000: 182 us, 212 without).
 #include "kv_step.h"
 #include "kv_tile.h"
 
@@ -51,7 +54,36 @@ __global__ __launch_bounds__(kShareThreads) void k_kv_share(const KvShareArgs A)
     A.plan[A.n_groups + i] = i >= g0 && i < g1 ? shared : 0;
 }
 
+// One workgroup for 256 / (D / 4) heads of a row: the parts of its states, in their order, become the first.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_state_join(const KvSharedArgs A) {
+  static_assert(WAVE % (D / 4) == 0, "a row's head is one wave's: its state is read before it is replaced");
+  const int across = (A.heads * (D / 4) + 255) / 256, row = blockIdx.x / across;
+  int local;
+  const int i = slot_owner(A.c, row, 1, 1, 0, local);
+  const KvSeq s = kv_seq(A.c, i);
+  if (row < s.row0 || row >= s.row0 + s.rows) return;
+  const int shared = shared_of(A, A.n_groups + i), parts = shared > 0 ? parts_of(A, shared) : 0;
+  if (parts < 2) return;
+  const int k = (int)(blockIdx.x % across) * 256 + threadIdx.x, head = k / (D / 4), d = 4 * (k % (D / 4));
+  if (head >= A.heads) return;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  RowState a{-INFINITY, -INFINITY, 0.0f};
+  join_state<D>(A, parts, row, head, d, v, a);
+  put_state<D>(A, 0, row, head, d, v, a);
+}
+
 }  // namespace
+
+hipError_t launch_kv_state_join(const KvSharedArgs& a, hipStream_t s) {
+  const long long grid = (long long)a.c.rows * ((a.heads * (a.c.dim / 4) + 255) / 256);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (a.c.dim == 128)
+    hipLaunchKernelGGL((k_kv_state_join<128>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_kv_state_join<64>), dim3((unsigned)grid), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
 
 hipError_t launch_kv_share(const KvShareArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(k_kv_share, dim3((unsigned)a.n_groups), dim3(kShareThreads), 0, s, a);

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
     int tries[kTries], got[kTries];
 #pragma unroll
     for (int e = 0; e < kTries; ++e) {
-      tries[e] = max((int)(((long long)total * (4 + e) + 4 * G - 1) / (4 * G)), kStepGrain);
+      tries[e] = max((int)(((long long)total * (4 + e) + 4 * G - 1) / (4 * G)), MODE == ATTEND_OWN ? kOwnGrain : kStepGrain);
       got[e] = pieces_of(mine.blocks, tries[e]);
     }
     for (int base = WAVE; base < items; base += WAVE) {
@@ -385,11 +385,11 @@ __global__ __launch_bounds__(WAVE* step_waves(NT, D), step_groups(NT, D) * step_
       f32x4 v = u;
       RowState a = of;
       if constexpr (MODE == ATTEND_SHARED) {
-        put_state<D>(A, row0 + j, h, d, v, a);
+        put_state<D>(A, 0, row0 + j, h, d, v, a);
         return;
       }
       if constexpr (MODE == ATTEND_OWN)
-        if (shared > 0) join_state<D>(A, row0 + j, h, d, v, a);
+        if (shared > 0) join_state<D>(A, parts_of(A, shared), row0 + j, h, d, v, a);
       T* out = static_cast<T*>(A.out.data) + (int64_t)(row0 + j) * A.out.token + (int64_t)h * A.out.head + d;
       const float half = out_half(a);
       typedef T T4 __attribute__((ext_vector_type(4)));

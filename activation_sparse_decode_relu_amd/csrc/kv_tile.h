@@ -30,7 +30,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kTileWaves = 4, kTileThreads = kTileWaves * WAVE;
 static_assert(kTileRows == 32 * kTileWaves, "a wave takes 32 rows");
-constexpr int kMinTiles = 4;    // 64-token tiles a split is worth at least
 
 // One workgroup's rows, tokens and share of them.
 struct TileJob {
@@ -79,7 +78,7 @@ __device__ __forceinline__ bool tile_job(const AttendArgs<MODE>& A, int slot, in
   j.span = item_span<MODE>(A, j.s.len, j.shared, j.pos(j.r0, A.group), j.pos(min(j.R, j.r0 + kTileRows) - 1, A.group));
   if (j.s.seq < 0) j.span = Span{0, 0, 0};
   const int tiles = (j.span.count() + 1) / 2;
-  const int per = max((tiles + A.splits - 1) / A.splits, kMinTiles);
+  const int per = tiles_each(tiles, A.splits);
   j.splits = max((tiles + per - 1) / per, 1);
   j.begin = split * per;
   j.end = min(j.begin + per, tiles);
@@ -311,6 +310,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const AttendArgs<MO
   // ---- out: register 4 a + e of o[d] is dim 32 d + 8 a + 4 h + e ---------------------------------------
   st.l += __shfl_xor(st.l, 32);
   if (!live) return;
+  if constexpr (MODE == ATTEND_SHARED) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+        put_state<D>(A, split, job.s.row0 + j, hq, 32 * d + 8 * a + 4 * h,
+                     f32x4{o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]}, st);
+    return;
+  }
   if (job.splits > 1) {
     float* to = A.partial + (((size_t)slot * c.kv_heads + head) * A.splits + split) * ((size_t)kTileRows * (D + 4)) +
                 (size_t)(32 * wave + col) * (D + 4);
@@ -323,15 +331,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const AttendArgs<MO
     if (h == 0) *reinterpret_cast<f32x4*>(to + D) = f32x4{st.rr, st.mm, st.l, 0.f};
     return;
   }
-  if constexpr (MODE == ATTEND_SHARED) {
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-        put_state<D>(A, job.s.row0 + j, hq, 32 * d + 8 * a + 4 * h,
-                     f32x4{o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]}, st);
-    return;
-  }
   if constexpr (MODE == ATTEND_OWN)
     if (job.shared > 0) {
       RowState joined = st;
@@ -341,7 +340,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void k_kv_tile(const AttendArgs<MO
         for (int a = 0; a < 4; ++a) {
           f32x4 v = {o[d][4 * a], o[d][4 * a + 1], o[d][4 * a + 2], o[d][4 * a + 3]};
           joined = st;
-          join_state<D>(A, job.s.row0 + j, hq, 32 * d + 8 * a + 4 * h, v, joined);
+          join_state<D>(A, parts_of(A, job.shared), job.s.row0 + j, hq, 32 * d + 8 * a + 4 * h, v, joined);
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[d][4 * a + e] = v[e];
         }
@@ -398,12 +397,8 @@ __global__ __launch_bounds__(kTileThreads) void k_kv_tile_join(const AttendArgs<
       }
   }
   const int j = r / A.group, hq = head * A.group + r - j * A.group;
-  if constexpr (MODE == ATTEND_SHARED) {
-    put_state<D>(A, job.s.row0 + j, hq, d, v, a);
-    return;
-  }
   if constexpr (MODE == ATTEND_OWN)
-    if (job.shared > 0) join_state<D>(A, job.s.row0 + j, hq, d, v, a);
+    if (job.shared > 0) join_state<D>(A, parts_of(A, job.shared), job.s.row0 + j, hq, d, v, a);
   T* out = static_cast<T*>(A.out.data) + (int64_t)(job.s.row0 + j) * A.out.token + (int64_t)hq * A.out.head + d;
   const float half = out_half(a);
   T4 w;
@@ -418,10 +413,11 @@ hipError_t tile_go(AttendArgs<MODE> a, hipStream_t s) {
   const long long slots = (long long)a.c.rows * a.group / kTileRows + items_of<MODE>(a), items = slots * a.c.kv_heads;
   if (items > 0x7fffffff) return hipErrorInvalidValue;
   a.slots = (int)slots;
-  a.splits = items > kTileParts / 2 ? 1 : (int)(kTileParts / items);
+  if constexpr (MODE == ATTEND_SHARED) a.splits = a.parts;
+  else a.splits = items > kTileParts / 2 ? 1 : (int)(kTileParts / items);
   hipLaunchKernelGGL((k_kv_tile<MODE, ACT, CODE, D>), dim3((unsigned)(items * a.splits)), dim3(kTileThreads), 0, s, a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
+  if (e != hipSuccess || a.splits == 1 || MODE == ATTEND_SHARED) return e;
   hipLaunchKernelGGL((k_kv_tile_join<MODE, ACT, D>), dim3((unsigned)items, kTileRows / join_rows(D)), dim3(kTileThreads), 0, s,
                      a);
   return hipGetLastError();

@@ -417,11 +417,19 @@ class KVCache:
         self._run(LIB.pi_kv_share, self._live(), _byref(batch), groups.data_ptr(), count, plan.data_ptr(),
                   self._stream(stream, (seqs, starts, groups, plan)))
 
+    def state_floats(self, rows) -> int:
+        """Elements of the fp32 scratch that attend_shared takes for `rows` rows."""
+        if rows >> 31:
+            _in32(rows=rows)
+        out = ctypes.c_size_t(0)
+        check(LIB.pi_kv_state_bytes(self._live(), rows, _byref(out)))
+        return int(out.value) // 4
+
     def attend_shared(self, layer, q, out, seqs, starts, groups, plan, max_new, max_rows, scale=None, lse=None, state=None,
                       stream=None) -> None:
         """attend (whole sequences, no window) for groups of sequences that begin with the same pages: what `plan` (share)
         says a group shares is read and multiplied once for all of its rows.  max_rows: at least the largest count of
-        rows of a group.  state: fp32 scratch of rows * heads * (head_dim + 4) elements, made here unless given."""
+        rows of a group.  state: fp32 scratch of state_floats(rows) elements, made here unless given."""
         d = self.desc
         n = self._ids(seqs, "seqs")
         self._ids(starts, "starts", n + 1)
@@ -436,7 +444,7 @@ class KVCache:
             _in32(layer=layer, rows=rows, max_new=max_new, max_rows=max_rows)
         handle = self._live()
         if state is None:
-            size = rows * d.heads * (d.head_dim + 4)
+            size = self.state_floats(rows)
             if stream is None:
                 state = torch.empty(size, dtype=torch.float32, device=self.device)
             else:   # of the stream that uses it

@@ -265,7 +265,8 @@ def test_strides_state_and_no_lse():
     f.cache.share(*ids, plan)
     want, lse = torch.empty(3, 8, 64, dtype=torch.float16, device="cuda"), torch.empty(3, 8, device="cuda")
     f.cache.attend_shared(0, qkv[:, :8].contiguous(), want, *ids, plan, 1, 3, lse=lse)
-    state = torch.full((3 * 8 * 68 + 4,), float("nan"), device="cuda")
+    need = f.cache.state_floats(3)
+    state = torch.full((need + 4,), float("nan"), device="cuda")
     out = torch.full((8, 4, 64), 7.0, dtype=torch.float16, device="cuda").transpose(0, 1)
     f.cache.attend_shared(0, qkv[:, :8], out[:3], *ids, plan, 1, 3, state=state)
     assert torch.equal(out[:3], want) and bool((out[3] == 7).all()) and bool(state[-4:].isnan().all())
