@@ -1,11 +1,15 @@
 """Decode steps of whole layers: attention over the 8-bit paged cache, then the sparse FFN.
 
     python examples/decode.py [--layers 8] [--seqs 8] [--prompt 500] [--tokens 64] [--window 0 --sinks 0] [--code e4m3]
+                              [--q4] [--rope] [--beams 1]
 
 Random weights and inputs (there is nothing to decode): each step's output, normalised, is the next step's input.
 The prompts go in by pieces; a step (room for a token, then per layer the projections, append, attend and the
 FFN) is captured once and replayed.  Then the second half of the sequences gives way to forks of the first, and the pool
 is compacted, as a beam search or a server does between steps.
+
+--q4 holds the attention's projections in 4 bits; --rope turns queries and keys by their positions and normalises them;
+--beams B runs B sequences on each prompt, which the attention then reads once for all of them.
 """
 
 import argparse
@@ -27,6 +31,15 @@ PIECE = 32   # tokens of a sequence in a piece of a prompt
 BATCH = 64   # tokens of an FFN call
 
 
+def four_bits(w):
+    """w [d_in][d_out] as the framework's product: a scale for 32 elements of a column, codes of -7 to 7."""
+    t = w.t().float().reshape(w.shape[1], -1, 32)
+    scales = (t.abs().amax(-1) / 7).half()
+    q = (t / scales.float().clamp(min=1e-7).unsqueeze(-1)).round().clamp(-8, 7).to(torch.int32) & 15
+    codes = (q[..., 0::2] | q[..., 1::2] << 4).to(torch.uint8).reshape(w.shape[1], -1)
+    return pi.Linear(codes.contiguous(), scales.contiguous(), act_dtype="f16")
+
+
 def norm(x):
     y = x.float()
     return (y * torch.rsqrt(y.square().mean(-1, keepdim=True) + 1e-6)).to(x.dtype)
@@ -37,7 +50,8 @@ class Decoder:
 
     heads, kv_heads, dim = 8, 2, 128
 
-    def __init__(self, layers, seqs, max_tokens, window=0, sinks=0, code="e4m3", page_tokens=64, mode="predicted", seed=0):
+    def __init__(self, layers, seqs, max_tokens, window=0, sinks=0, code="e4m3", page_tokens=64, mode="predicted", seed=0,
+                 q4=False, rope=False, beams=1):
         cfg = LayerConfig(name="decoder", cfg_id=9, workload="decoder d=1024 n=4096 r=128", d_model=1024, d_ffn=4096, rank=128,
                           gated=True, w_dtype="f16", p_dtype="f16", act_dtype="f16", n_layers=layers, tokens=1,
                           density=0.10, zipf_s=1.1)
@@ -52,20 +66,43 @@ class Decoder:
         self.qkv = [(torch.randn(self.d, width, device="cuda", generator=g) * self.d ** -0.5).half() for _ in range(layers)]
         self.proj = [(torch.randn(self.heads * self.dim, self.d, device="cuda", generator=g) * self.d ** -0.5).half()
                      for _ in range(layers)]
+        if q4:
+            self.qkv, self.proj = [four_bits(w) for w in self.qkv], [four_bits(w) for w in self.proj]
+        self.rope = pi.Rope(self.dim) if rope else None
+        if rope:
+            self.norms = [(1 + 0.1 * torch.randn(2, self.dim, device="cuda", generator=g)).half() for _ in range(layers)]
+        self.beams = beams
         per_seq = -(-max_tokens // page_tokens)
         self.cache = pi.KVCache(self.heads, self.kv_heads, self.dim, pages=seqs * (per_seq + 1), page_tokens=page_tokens,
                                 max_seqs=seqs, max_seq_pages=per_seq, code=code, layers=layers)
 
-    def run(self, x, seqs, counts, starts, max_new):
-        """The next counts[i] tokens of seqs[i], rows [starts[i], starts[i + 1]) of x [rows][d], through every layer."""
+    def product(self, w, x, add=None):
+        if not isinstance(w, pi.Linear):
+            return x @ w if add is None else add + x @ w
+        y = torch.empty(x.shape[0], w.desc.d_out, dtype=x.dtype, device=x.device)
+        w.forward(x, y, add=add)
+        return y
+
+    def run(self, x, seqs, counts, starts, max_new, groups=None):
+        """The next counts[i] tokens of seqs[i], rows [starts[i], starts[i + 1]) of x [rows][d], through every layer.
+        groups: where each set of self.beams sequences on one prompt begins."""
         rows, h, kv = x.shape[0], self.heads, self.kv_heads
         self.cache.reserve(seqs, counts)
+        if groups is not None:
+            plan = torch.empty(groups.numel() - 1 + seqs.numel(), dtype=torch.int32, device=x.device)
+            self.cache.share(seqs, starts, groups, plan)
         for i, ffn in enumerate(self.ffn):
-            t = (norm(x) @ self.qkv[i]).view(rows, h + 2 * kv, self.dim)
-            self.cache.append(i, t[:, h:h + kv], t[:, h + kv:], seqs, starts)
+            t = self.product(self.qkv[i], norm(x)).view(rows, h + 2 * kv, self.dim)
+            q, k = t[:, :h], t[:, h:h + kv]
+            if self.rope is not None:
+                self.cache.rotate(self.rope, q, q, k, k, seqs, starts, q_norm=self.norms[i][0], k_norm=self.norms[i][1])
+            self.cache.append(i, k, t[:, h + kv:], seqs, starts)
             out = torch.empty(rows, h, self.dim, dtype=x.dtype, device=x.device)
-            self.cache.attend(i, t[:, :h], out, seqs, starts, max_new, window=self.window, sinks=self.sinks)
-            x = x + out.view(rows, -1) @ self.proj[i]
+            if groups is not None:
+                self.cache.attend_shared(i, q, out, seqs, starts, groups, plan, max_new, self.beams * max_new)
+            else:
+                self.cache.attend(i, q, out, seqs, starts, max_new, window=self.window, sinks=self.sinks)
+            x = self.product(self.proj[i], out.view(rows, -1), x)
             y, z = norm(x), torch.empty_like(x)
             for at in range(0, rows, BATCH):
                 ffn.forward(y[at:at + BATCH], z[at:at + BATCH], self.mode)
@@ -73,22 +110,29 @@ class Decoder:
         return x
 
     def prompts(self, x):
-        """x [seqs][tokens][d], by pieces of PIECE tokens; returns the last token's output of each sequence."""
+        """x [prompts][tokens][d], by pieces of PIECE tokens, into the first of each prompt's sequences; returns the last
+        token's output of each sequence."""
         n, tokens, _ = x.shape
-        seqs = ints(range(n))
+        seqs = ints(range(0, n * self.beams, self.beams))
         for at in range(0, tokens, PIECE):
             piece = x[:, at:at + PIECE]
             c = piece.shape[1]
             y = self.run(piece.reshape(n * c, -1), seqs, ints([c] * n), ints(range(0, n * c + 1, c)), c)
-        return y.view(n, c, -1)[:, -1]
+        for j in range(1, self.beams):
+            self.cache.fork(seqs, seqs + j)
+        return y.view(n, c, -1)[:, -1].repeat_interleave(self.beams, 0)
+
+    def step(self):
+        """What run takes behind x for one token of every sequence."""
+        n = self.seqs
+        return ints(range(n)), ints([1] * n), ints(range(n + 1)), 1, ints(range(0, n + 1, self.beams)) if self.beams > 1 else None
 
     def capture(self, x):
         """A graph that takes one token of every sequence from x [seqs][d] and puts the output's norm back."""
-        n = self.seqs
-        self.step_ids = ints(range(n)), ints([1] * n), ints(range(n + 1))   # the graph reads them: they live as long as it
+        self.step_ids = self.step()   # the graph reads them: they live as long as it
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            x.copy_(norm(self.run(x, *self.step_ids, 1)))
+            x.copy_(norm(self.run(x, *self.step_ids)))
         return graph
 
 
@@ -100,17 +144,27 @@ def main():
     p = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     for name, value in (("layers", 8), ("seqs", 8), ("prompt", 500), ("tokens", 64), ("window", 0), ("sinks", 0)):
         p.add_argument(f"--{name}", type=int, default=value)
+    p.add_argument("--beams", type=int, default=1)
+    for name in ("q4", "rope"):
+        p.add_argument(f"--{name}", action="store_true")
     p.add_argument("--code", choices=("e4m3", "int8"), default="e4m3")
     a = p.parse_args()
     if not 2 <= a.seqs <= BATCH:
         p.error(f"--seqs must lie in [2, {BATCH}]")
-    model = Decoder(a.layers, a.seqs, a.prompt + 2 * a.tokens + 2, a.window, a.sinks, a.code)
+    if a.beams < 1 or a.seqs % a.beams:
+        p.error("--seqs must be a multiple of --beams")
+    if a.beams > 1 and (a.window or a.sinks):
+        p.error("--beams reads whole prompts: it takes no --window or --sinks")
+    model = Decoder(a.layers, a.seqs, a.prompt + 2 * a.tokens + 2, a.window, a.sinks, a.code, q4=a.q4, rope=a.rope,
+                    beams=a.beams)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
-    x = torch.randn(a.seqs, a.prompt, model.d, device="cuda", generator=g).half()
+    x = torch.randn(a.seqs // a.beams, a.prompt, model.d, device="cuda", generator=g).half()
     first = norm(model.prompts(x))
-    model.run(first.clone(), ints(range(a.seqs)), ints([1] * a.seqs), ints(range(a.seqs + 1)), 1)   # warms the libraries up
+    model.run(first.clone(), *model.step())   # warms the libraries up
     state = first.clone()
+    if a.beams > 1:   # beams of a prompt part from here on
+        state += 0.01 * torch.randn(a.seqs, model.d, device="cuda", generator=g).half()
     graph = model.capture(state)
 
     def steps(count):
