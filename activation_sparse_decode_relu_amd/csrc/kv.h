@@ -62,10 +62,14 @@ struct KvSharedArgs : KvAttendArgs {
   int n_groups;
   int parts;           // into how many parts a group's tokens are split at most (kernel of many rows), 1 for few rows
 };
-// Workgroups that the shared tokens are split for where there are many rows, and the parts that this makes.
+// Workgroups that the shared tokens are split for where there are many rows, and the parts that this makes.  Half as many
+// leave fewer parts to write and join but compute units idle: two layers of 64 sequences on 4096 tokens 99 us instead of 108, but
+// 4 sequences, 4 tokens each, on a document of 100003 295 instead of 243, and 2 x 4, 5 tokens each, on 20000 208 instead of 174.
 constexpr int kSharedParts = 512;
+// Tiles of 128 rows that as many groups have at most.
+constexpr long long shared_tiles(long long rows, int group, int n_groups) { return (rows * group + n_groups * 127ll) / 128; }
 constexpr int shared_parts(long long rows, int group, int kv_heads, int n_groups) {
-  const long long items = (rows * group / 128 + n_groups) * kv_heads;
+  const long long items = shared_tiles(rows, group, n_groups) * kv_heads;
   return items > kSharedParts / 2 ? 1 : (int)(kSharedParts / items);
 }
 struct KvShareArgs {
@@ -81,9 +85,9 @@ hipError_t launch_kv_step_shared(int act, int code, int mode, const KvSharedArgs
 hipError_t launch_kv_tile_shared(int act, int code, int mode, const KvSharedArgs& a, hipStream_t s);
 
 // Few rows of a cached head (max_new * group up to kStepRows): items (sequences times cached heads) in pieces, one
-// workgroup each, see kv_step.hip.  S is at least kStepGrain blocks.
-// (Behind shared tokens items are short, and a part to join costs more than some 24 blocks: 64 sequences of 30 to 800 own tokens,
-// 8 heads, 108 us for two layers with 32, 123 with 8.)
+// workgroup each, see kv_step.h.  S is at least kStepGrain blocks.
+// (Behind shared tokens items are short, and a part to join costs more than some 24 blocks: two layers of 64 sequences on
+// 4096 shared tokens, 8 cached heads, 108 us with 32, 123 with 8.)
 constexpr int kStepRows = 64, kStepGrain = 8, kOwnGrain = 32;
 // tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.  Eight
 // waves instead of four where 33 to 64 rows have 64 dims: half as many parts to join (four tokens over 100003, 16

@@ -65,7 +65,8 @@ __device__ __forceinline__ Span item_span(const AttendArgs<MODE>& A, int len, in
   return s;
 }
 
-// slot_owner() over items.
+// slot_owner() over items.  Groups begin their slots at floor((rows before - i) / unit) + i: as many as a unit's
+// rounding up needs, and no more with one group.
 template <int MODE>
 __device__ __forceinline__ int item_owner(const AttendArgs<MODE>& A, int slot, int unit, int& local) {
   if constexpr (MODE != ATTEND_SHARED) return slot_owner(A.c, slot, A.group, unit, 1, local);
@@ -74,7 +75,8 @@ __device__ __forceinline__ int item_owner(const AttendArgs<MODE>& A, int slot, i
   local = slot;
   for (int base = 0; base < items; base += WAVE) {
     const int i = base + lane;
-    const long long at = i < items ? (long long)item_start<MODE>(A, i) * A.group / unit + i : 0x7fffffffffffll;
+    const long long at = i < items ? ((long long)item_start<MODE>(A, i) * A.group + (long long)i * (unit - 1)) / unit
+                                   : 0x7fffffffffffll;
     const unsigned long long le = __ballot(at <= slot);
     if (le == 0) break;
     const int last = 63 - __builtin_clzll(le);

@@ -14,6 +14,11 @@
 // 328 us).  So there code times scale is an fp16 operand, rounded to half a step of 2^-11, no more than an fp16 y itself
 // is, and the sums stay in 32x32x16 products.  bf16 rows are made fp16 for this, each by a power of two of its own, in the
 // caller's scratch: what is lost lies 2^-39 below a row's largest.
+//
+// Measured (codes and scales read once at 6.99 TB/s; products at a library's 1166 to 1223 TFLOP/s): 1 row 8192 -> 10240 10.0 us
+// (6.8); 16 rows 8192 -> 8192 11.3 to 12.4 (5.5); 64 rows 7168 -> 21504 45 to 47 (12.9; products 16.1), where each workgroup reads all of x
+// from its L2, the vector ALU is busy 37 % of the time and the matrix instructions 20 %; 2000 rows 4096 -> 12288 232 (products 173;
+// the library's own fp16 product of this size takes 187), the vector ALU busy 58 % and the matrix instructions 48 %.
 #include "kv_linear.h"
 #include "kv_softmax.h"
 

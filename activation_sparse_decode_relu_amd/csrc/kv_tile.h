@@ -49,7 +49,11 @@ template <int MODE>
 __device__ __forceinline__ int sorted_owner(const AttendArgs<MODE>& A, int slot, int& local) {
   const int items = items_of<MODE>(A), lane = threadIdx.x & (WAVE - 1), i = min(lane, items - 1);
   auto lane_of = [](int v, int k) { return __builtin_amdgcn_readlane(v, k); };
-  auto at = [&](int k) { return (int)((long long)item_start<MODE>(A, k) * A.group / kTileRows); };
+  auto at = [&](int k) {   // less k
+    const long long r = (long long)item_start<MODE>(A, k) * A.group;
+    if constexpr (MODE == ATTEND_SHARED) return (int)((r + (long long)k * (kTileRows - 1)) / kTileRows) - k;
+    else return (int)(r / kTileRows);
+  };
   const int count = max(at(i + 1) + 1 - at(i), 0), len = item_seq<MODE>(A, i).len;
   int before = 0;
   for (int k = 0; k < items; ++k) {
@@ -410,7 +414,9 @@ __global__ __launch_bounds__(kTileThreads) void k_kv_tile_join(const AttendArgs<
 
 template <int MODE, int ACT, int CODE, int D>
 hipError_t tile_go(AttendArgs<MODE> a, hipStream_t s) {
-  const long long slots = (long long)a.c.rows * a.group / kTileRows + items_of<MODE>(a), items = slots * a.c.kv_heads;
+  const long long slots = MODE == ATTEND_SHARED ? shared_tiles(a.c.rows, a.group, items_of<MODE>(a))
+                                                : (long long)a.c.rows * a.group / kTileRows + items_of<MODE>(a);
+  const long long items = slots * a.c.kv_heads;
   if (items > 0x7fffffff) return hipErrorInvalidValue;
   a.slots = (int)slots;
   if constexpr (MODE == ATTEND_SHARED) a.splits = a.parts;
