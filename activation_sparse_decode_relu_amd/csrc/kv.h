@@ -69,6 +69,7 @@ constexpr int kSharedParts = 512;
 // Tiles of 128 rows that as many groups have at most.
 constexpr long long shared_tiles(long long rows, int group, int n_groups) { return (rows * group + n_groups * 127ll) / 128; }
 constexpr int shared_parts(long long rows, int group, int kv_heads, int n_groups) {
+  if (rows < 1) return 1;
   const long long items = shared_tiles(rows, group, n_groups) * kv_heads;
   return items > kSharedParts / 2 ? 1 : (int)(kSharedParts / items);
 }
