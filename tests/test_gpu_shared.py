@@ -361,3 +361,24 @@ def test_another_stream():
         torch.cuda.synchronize()
         outs.append(out)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("times", [1, 10])
+@pytest.mark.parametrize("order", [1, -1])
+def test_rows_that_fill_tiles(times, order):
+    """Groups whose rows end at, before and behind 128 of them, or that have none: up to 64 groups and more."""
+    announce(f"shared, rows that fill tiles, {times} times, {order}")
+    counts = [(64, 63), (64, 64), (65, 64), (0, 0), (128, 127), (128, 128), (128, 129), (0, 0), (0, 0), (66, 0), (0, 1)][::order] * times
+    f = Family([64] * len(counts), [[max(c, 1) for c in pair] for pair in counts], 1, 1, 64, 32, "f16", "e4m3", seed=7)
+    f.step([c for pair in counts for c in pair])
+
+
+def test_no_rows():
+    announce("shared, no rows")
+    f = Family([64], [[1, 1]], 4, 2, 64, 32)
+    assert f.cache.state_floats(0) == 0
+    f.cache.share(_ids([0, 1]), _ids([0, 0, 0]), _ids([0, 2]), plan := torch.zeros(3, dtype=torch.int32, device="cuda"))
+    q = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")
+    f.cache.attend_shared(0, q, q.clone(), _ids([0, 1]), _ids([0, 0, 0]), _ids([0, 2]), plan, 0, 0)
+    torch.cuda.synchronize()
+    assert plan.tolist() == [64, 64, 64]
