@@ -10,8 +10,8 @@
 // angles are worked out once.
 //
 // Bound by reading and writing q and k once, a step by its launch: 4096 tokens of 32 + 32 heads of 128 dims, bf16, 134 MB,
-// 26.6 us (a large copy runs at 4.88 TB/s); five pieces of prompts, 128 + 8 heads of 64 dims with norms and 32 of them turned,
-// 59 MB, 19.4 us; 64 tokens of 64 + 8 heads 5.2 us.
+// 23.6 us (5.7 TB/s; a large copy runs at 4.88, and the last cache holds part of these); five pieces of prompts, 128 + 8 heads of 64 dims with norms and 32 of them turned,
+// 59 MB, 17.3 us; 64 tokens of 64 + 8 heads 5.2 us.
 #include "kv_device.h"
 #include "kv_rotate.h"
 
@@ -137,9 +137,20 @@ hipError_t rotate_go(const KvRotateArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// A wave's position and angles serve more heads where there are waves enough without: by one, two or four times its
+// heads, 64 tokens of 64 + 8 heads of 128 dims (1152 waves) take 4.5, 4.6 and 5.4 us, 300 (5400) 7.3, 6.3 and 6.6, 800 (14400)
+// 13.6, 10.6 and 9.8, and 2000 28.2, 21.7 and 21.0.
+template <int ACT, int D, int LAYOUT>
+hipError_t rotate_any(const KvRotateArgs& a, hipStream_t s) {
+  constexpr int kHeads = WAVE / (D / 8), kSimds = 1024, kFull = 8 * kSimds;
+  const long long waves = (long long)a.c.rows * ((a.heads + a.c.kv_heads + kHeads - 1) / kHeads);
+  if (waves < 2 * kSimds) return rotate_go<ACT, D, LAYOUT, 1>(a, s);
+  return waves < kFull ? rotate_go<ACT, D, LAYOUT, 2>(a, s) : rotate_go<ACT, D, LAYOUT, 4>(a, s);
+}
+
 template <int ACT, int D>
 hipError_t rotate_layout(int layout, const KvRotateArgs& a, hipStream_t s) {
-  return layout == ROPE_HALF ? rotate_go<ACT, D, ROPE_HALF, 1>(a, s) : rotate_go<ACT, D, ROPE_INTERLEAVED, 1>(a, s);
+  return layout == ROPE_HALF ? rotate_any<ACT, D, ROPE_HALF>(a, s) : rotate_any<ACT, D, ROPE_INTERLEAVED>(a, s);
 }
 
 }  // namespace

@@ -240,3 +240,14 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         r.compare(qo, q, [49 + step, 59 + step], qn)
         r.compare(ko, k, [49 + step, 59 + step], kn)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("heads, kvh, dim", [(30, 5, 128), (33, 11, 64), (13, 13, 128)])
+@pytest.mark.parametrize("counts", [[250, 1, 0, 40], [900, 3, 1, 500]])
+def test_several_heads_a_wave(counts, heads, kvh, dim, layout):
+    """Calls in which a wave takes two and four times its heads, with heads left over; with norms, without, and a part turned."""
+    announce(f"rotate {counts} {heads} {kvh} {dim} {layout}")
+    r = Rig([5000, 70, 9, 501], heads, kvh, dim, "f16", layout=layout, rot_dims=dim // 2, seed=heads)
+    r.run(counts)
+    r.run(counts, norm=False)
