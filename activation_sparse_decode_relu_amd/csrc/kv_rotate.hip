@@ -10,8 +10,8 @@
 // angles are worked out once.
 //
 // Bound by reading and writing q and k once, a step by its launch: 4096 tokens of 32 + 32 heads of 128 dims, bf16, 134 MB,
-// 23.6 us (5.7 TB/s; a large copy runs at 4.88, and the last cache holds part of these); five pieces of prompts, 128 + 8 heads of 64 dims with norms and 32 of them turned,
-// 59 MB, 17.3 us; 64 tokens of 64 + 8 heads 5.2 us.
+// 23.6 us (5.7 TB/s; a large copy runs at 4.88, and the last cache holds part of these); five pieces of prompts, 128 + 8
+// heads of 64 dims with norms and 32 of them turned, 59 MB, 17.3 us; 64 tokens of 64 + 8 heads 5.2 us.
 #include "kv_device.h"
 #include "kv_rotate.h"
 

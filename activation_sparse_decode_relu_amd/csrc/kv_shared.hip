@@ -10,8 +10,9 @@
 // (two layers of 2 x 4 sequences, 80 rows of a head, on 20000: 174 us; 212 without, where the first launch took 9 us more).
 //
 // The first launch is bound as its kernel is: by the vector ALU and the matrix instructions for many rows (4 sequences, 4
-// tokens each, 128 heads on 8 of 64 dims in int8, on 100003 tokens: 97 us, their products alone 45 at a library product's rate), by latency for few.  The second is bound by reading codes and states, and
-// at its start and end (64 sequences of 30 to 800 own tokens, 8 heads of 128: 20 to 23 us for 54 MB of codes and 31 of states).
+// tokens each, 128 heads on 8 of 64 dims in int8, on 100003 tokens: 97 us, their products alone 45 at a library product's
+// rate), by latency for few.  The second is bound by reading codes and states, and at its start and end (64 sequences of 30
+// to 800 own tokens, 8 heads of 128: 20 to 23 us for 54 MB of codes and 31 of states).
 #include "kv_step.h"
 #include "kv_tile.h"
 
