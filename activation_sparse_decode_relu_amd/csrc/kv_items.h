@@ -58,10 +58,11 @@ __device__ __forceinline__ int item_first(const KvSeq& s) {
 }
 
 template <int MODE>
-__device__ __forceinline__ Span item_span(const AttendArgs<MODE>& A, int len, int shared, int p0, int p1) {
+__host__ __device__ __forceinline__ Span item_span(const AttendArgs<MODE>& A, int len, int shared, int p0, int p1) {
   if constexpr (MODE == ATTEND_SHARED) return Span{0, 0, len / kKvBlock};
   Span s = span_of(p0, p1, A.window, A.sinks);
-  if constexpr (MODE == ATTEND_OWN) s.from = min(shared / kKvBlock, s.end);
+  // at the last block, where a plan that does not fit says more: the block behind it may lie past the table
+  if constexpr (MODE == ATTEND_OWN) s.from = min(shared / kKvBlock, max(s.end - 1, 0));
   return s;
 }
 

@@ -139,10 +139,10 @@ __device__ __forceinline__ float query_scale(float amax, float& inverse) {
 // to `end`; p0 and p1 are the first and last position of the rows in question.
 struct Span {
   int sink, from, end;
-  __device__ __forceinline__ int count() const { return sink + end - from; }
-  __device__ __forceinline__ int block(int i) const { return i < sink ? i : from + (i - sink); }
+  __host__ __device__ __forceinline__ int count() const { return sink + end - from; }
+  __host__ __device__ __forceinline__ int block(int i) const { return i < sink ? i : from + (i - sink); }
 };
-__device__ __forceinline__ Span span_of(int p0, int p1, int window, int sinks) {
+__host__ __device__ __forceinline__ Span span_of(int p0, int p1, int window, int sinks) {
   Span s{0, 0, p1 < 0 ? 0 : p1 / kKvBlock + 1};
   if (window > 0 && p0 >= window) {
     s.from = min((p0 - window + 1) / kKvBlock, s.end);

@@ -382,3 +382,21 @@ def test_no_rows():
     f.cache.attend_shared(0, q, q.clone(), _ids([0, 1]), _ids([0, 0, 0]), _ids([0, 2]), plan, 0, 0)
     torch.cuda.synchronize()
     assert plan.tolist() == [64, 64, 64]
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_plan_past_a_full_sequence(new):
+    """A plan that says more than a sequence which fills its row of the table holds: the other group's rows are right."""
+    announce(f"shared, plan past a full sequence, {new} new")
+    f = Family([96, 96], [[new, new], [new, new]], 4, 2, 64, 32, "f16", "e4m3", seed=18)
+    f.cache.lens[2:] = f.cache.table.shape[1] * 32
+    before = {name: getattr(f.cache, name).clone() for name in ("k", "v", "table", "lens", "refs")}
+    q = torch.randn(4 * new, 4, 64).half()
+    out, lse = torch.empty(4 * new, 4, 64, dtype=torch.float16, device="cuda"), torch.empty(4 * new, 4, device="cuda")
+    for much in (1 << 20, 0x7fffffff):
+        f.cache.attend_shared(0, q.cuda(), out, _ids(range(4)), _ids(range(0, 4 * new + 1, new)), _ids([0, 2, 4]),
+                              _ids([96, much, 96, 96, much, much]), new, 2 * new, lse=lse)
+        torch.cuda.synchronize()
+        f.compare(q[:2 * new], out[:2 * new], lse[:2 * new], [0, new, 2 * new], [0, 1], 0, 0, None)
+        for name, t in before.items():
+            assert torch.equal(t, getattr(f.cache, name))

@@ -1,6 +1,7 @@
 """Attention of groups that share their beginning, without a GPU: refusals of the C ABI and of the binding."""
 
 import ctypes
+import subprocess
 
 import pytest
 
@@ -102,3 +103,36 @@ def test_share_binding():
         with pytest.raises(pi.PiError) as e:
             _cache().share(_ints(3), _ints(4), groups, plan)
         assert needle in str(e.value)
+
+
+# ---- which blocks the kernel of few rows looks up --------------------------------------------------------
+
+SPANS = r"""
+#include "kv_items.h"
+
+// Lanes look up blocks 0 .. 63 of a sequence's span, the last again where there are fewer: none may lie past the table's
+// columns, whatever the plan says, and with a plan that fits, the span is what the sequence holds behind it.
+int main() {
+  pik::KvSharedArgs A{};
+  const int cap = 4;   // blocks that the table has room for
+  for (int len = 0; len <= 32 * cap; ++len)
+    for (int rows = 1; rows <= len + 3; ++rows)
+      for (int shared = 0; shared <= 32 * cap; shared += 32) {
+        const pik::Span s = pik::item_span<pik::ATTEND_OWN>(A, len, shared, len - rows, len - 1);
+        for (int lane = 0; lane < 64; ++lane) {
+          const int last = s.count() > 0 ? s.count() - 1 : 0, block = s.block(lane < last ? lane : last);
+          if (block < 0 || block >= cap) return 1;
+        }
+        if (shared <= len - rows && (s.block(0) != shared / 32 || s.end != (len + 31) / 32)) return 2;
+      }
+  return 0;
+}
+"""
+
+
+def test_no_block_past_the_table(tmp_path):
+    from activation_sparse_decode_relu_amd._build import CSRC, hipcc
+    (tmp_path / "spans.hip").write_text(SPANS)
+    subprocess.run([hipcc(), "--cuda-host-only", "-std=c++17", "-O1", "-I", CSRC, str(tmp_path / "spans.hip"), "-o",
+                    str(tmp_path / "spans")], check=True, timeout=100)
+    assert subprocess.run([str(tmp_path / "spans")], timeout=20).returncode == 0
