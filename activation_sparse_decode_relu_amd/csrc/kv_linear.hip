@@ -64,8 +64,11 @@ __device__ __forceinline__ typename ActT<ACT>::V8 operand(unsigned w, unsigned o
 
 // ---- laying out ----------------------------------------------------------------------------------------
 
-// One wave a row of scales: the power of two that brings the largest to [8, 16).  So products of codes and scales stay in
-// fp16's normal range whatever the row's size is.
+// One wave a row of scales: the power of two that they are divided by.  It brings a largest below 8 to [8, 16), so that most
+// products of codes and scales are normal in fp16, and takes one of 2^13 and more below that, since -8 times it has to be
+// finite (8 * 8188 = 65504).  Only the latter, by up to 8, can cost a scale bits: those below 2^-11 beside one of 2^13.  All
+// others are multiples of fp16's smallest value after it as they were before, and so is code times scale where it is subnormal.
+// (With every largest brought to [8, 16) a scale 2^-28 of it became 0, and was missing where x is 0 beside the large ones.)
 __global__ __launch_bounds__(256) void k_linear_factor(const unsigned short* __restrict__ scales, float* __restrict__ factor,
                                                        int groups, int d_out, int padded) {
   const int row = blockIdx.x * (256 / WAVE) + threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
@@ -77,7 +80,7 @@ __global__ __launch_bounds__(256) void k_linear_factor(const unsigned short* __r
 #pragma unroll
   for (int m = 1; m < WAVE; m <<= 1) top = fmaxf(top, __shfl_xor(top, m));
   const int x = (int)(__builtin_bit_cast(unsigned, top) >> 23) - 127;   // top in [2^x, 2^(x + 1)), exact in fp32
-  if (lane == 0) factor[row] = top > 0.0f && top <= 65504.0f ? pow2i(x - 3) : 1.0f;
+  if (lane == 0) factor[row] = top > 0.0f && top <= 65504.0f ? pow2i(min(x - 3, max(x - 12, 0))) : 1.0f;
 }
 
 // One wave a slab.

@@ -14,8 +14,9 @@
  * scales [16 rows][8 groups].  Word j of the 16 bytes 16 l .. of a KB holds the columns 32 j + 8 (l / 16) .. + 8
  * of row l % 16, as u = q + 8: column 2 i at bit 4 i and column 2 i + 1 at bit 16 + 4 i, the word rotated left
  * by 6 bits.  Rows and columns that are not there have q = 0 and scale 0.  Behind the
- * slabs stands a power of two for each row (fp32) that its scales were divided by, which brings the largest of them to
- * [8, 16); what a scale 2^-17 of that and less loses lies under the sums' own rounding.
+ * slabs stands a power of two for each row (fp32) that its scales were divided by: less than 1 where the largest is below 8,
+ * and up to 8 where it is 2^13 or more.  Scales are kept as they are, except beside one of 2^13 and more: there those below
+ * 2^-11 are rounded to a multiple of up to 2^-21.
  *
  * Conventions (as in pi_ffn.h: status codes, pi_last_error, host checks before anything is enqueued)
  * --------------------------------------------------------------------------------------------------

@@ -295,3 +295,33 @@ def test_weights_past_4_gib(rows):
     m.forward(x.cuda(), y)
     want = x.double() @ torch.from_numpy(q.astype(np.float64)).T
     assert bool((y[:, :-tail] == 0).all()) and torch.equal(y[:, -tail:].cpu(), want.half())
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [1, 3, 16, 24, 64, 100])
+def test_small_scales_beside_large_ones(rows, act):
+    """x is zero where a row's largest scale is: what the small ones bring is all there is.  Codes and x are powers of two, so
+    each output is one exact product, with scales of all of fp16's bits, unless the row's largest is 2^13 or more: its scales
+    are divided by up to 8 and may lose half a step of 2^-24 of that."""
+    announce(f"linear small scales {rows} {act}")
+    import activation_sparse_decode_relu_amd as pi
+    rng = np.random.default_rng(rows)
+    groups, tops = 12, np.arange(-24, 16)
+    d_out = 2 * len(tops)
+    q = np.zeros((d_out, 32 * groups), dtype=np.int64)
+    scales = np.exp2(rng.integers(-24, np.repeat(tops, 2)[:, None] + 1, (d_out, groups))) * (1 + rng.integers(0, 1024, (d_out, groups)) / 1024)
+    scales[:, 0] = np.exp2(np.repeat(tops, 2))
+    scales = np.minimum(scales, 1.999 * scales[:, :1]).astype(np.float16)
+    q[:, ::32] = rng.choice([-8, -4, -2, -1, 1, 2, 4], (d_out, groups))
+    m = pi.Linear(torch.from_numpy(pack_nibbles(q)).cuda(), torch.from_numpy(scales).cuda(), act_dtype=act)
+    x = np.zeros((rows, 32 * groups))
+    at = rng.integers(1, groups, rows)
+    x[np.arange(rows), 32 * at] = np.exp2(rng.integers(-2, 3, rows))
+    y = torch.empty(rows, d_out, dtype=DT[act], device="cuda")
+    m.forward(torch.from_numpy(x).to(DT[act]).cuda(), y)
+    want = torch.from_numpy(x @ (q * np.repeat(scales.astype(np.float64), 32, axis=1)).T)
+    exact = torch.from_numpy(scales.max(1) < 8192)
+    assert torch.equal(y.cpu()[:, exact], want.to(DT[act])[:, exact])
+    want = want.clamp(-float(torch.finfo(DT[act]).max), float(torch.finfo(DT[act]).max))
+    err = (y.cpu().double().clamp(-float(torch.finfo(DT[act]).max), float(torch.finfo(DT[act]).max)) - want).abs()
+    assert bool((err <= EPS[act] * want.abs() + TINY[act] + 2.0 ** -22 * 8 * x.max()).all())
