@@ -656,7 +656,7 @@ hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
     return a.tiles <= 1024 ? rows_go<ACT, 4, 2, 4, 2, 1>(a, s) : rows_go<ACT, 4, 3, 4, 2, 1>(a, s);
   }
   LinearArgs b = a;
-  const LinearScratch layout = linear_scratch(ACT, a.rows, a.d_in, a.d_out);
+  const LinearScratch layout = linear_scratch(ACT, a.rows, a.d_in, a.d_out, a.scratch_bytes);
   char* scratch = static_cast<char*>(a.scratch);
   b.splits = layout.splits;
   b.partial = reinterpret_cast<float*>(scratch + layout.partial);

@@ -94,6 +94,14 @@ pi_status pi_linear_scratch_bytes(const pi_linear* h, int32_t rows, size_t* byte
   return ok();
 }
 
+pi_status pi_linear_scratch_bytes_upto(const pi_linear* h, int32_t rows, size_t* bytes) {
+  if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
+  if (bytes == nullptr) return fail(PI_ERR_INVALID, "bytes is NULL");
+  if (rows < 0 || rows > kMaxRows) return fail(PI_ERR_INVALID, "rows=%d must lie in [0, %d]", rows, kMaxRows);
+  *bytes = pik::linear_scratch_upto(h->desc.act_dtype, rows, h->desc.d_in, h->desc.d_out);
+  return ok();
+}
+
 pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stream) {
   if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
   if (args == nullptr) return fail(PI_ERR_INVALID, "args is NULL");
@@ -109,11 +117,14 @@ pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stre
     return fail(PI_ERR_INVALID, "add_stride=%lld must not be negative", (long long)args->add_stride);
   if (args->rows > 1 && args->y_stride < d.d_out)
     return fail(PI_ERR_INVALID, "y_stride=%lld is less than d_out=%d", (long long)args->y_stride, d.d_out);
-  const size_t need = pik::linear_scratch(d.act_dtype, args->rows, d.d_in, d.d_out).total;
-  if (need > 0 && (args->scratch == nullptr || !aligned(args->scratch, 16) || args->scratch_bytes < need))
-    return fail(PI_ERR_WORKSPACE, "scratch must be %zu bytes, 16-byte aligned", need);
+  const size_t given = args->scratch != nullptr ? args->scratch_bytes : 0;
+  const size_t need = pik::linear_scratch(d.act_dtype, args->rows, d.d_in, d.d_out, given).total;
+  if (need > 0 && (!aligned(args->scratch, 16) || given < need))
+    return fail(PI_ERR_WORKSPACE, "scratch must be at least %zu bytes, 16-byte aligned",
+                pik::linear_scratch(d.act_dtype, args->rows, d.d_in, d.d_out, 0).total);
   pik::LinearArgs a{};
   a.scratch = args->scratch;
+  a.scratch_bytes = given;
   a.packed = h->packed;
   a.factor = h->factor();
   a.bias = h->bias;

@@ -14,12 +14,12 @@ import torch
 from .binding import LIB, _invalid, check
 
 PI_LINEAR_F16, PI_LINEAR_BF16 = range(2)
-LINEAR_ABI_VERSION = 1   # PI_LINEAR_ABI_VERSION of the header this binding follows
+LINEAR_ABI_VERSION = 2   # PI_LINEAR_ABI_VERSION of the header this binding follows
 LINEAR_ACTS = {"f16": PI_LINEAR_F16, "bf16": PI_LINEAR_BF16}
 _ACT_TORCH = {PI_LINEAR_F16: torch.float16, PI_LINEAR_BF16: torch.bfloat16}
 
 LINEAR_EXPORTED = ("pi_linear_abi_version", "pi_linear_packed_bytes", "pi_linear_create", "pi_linear_destroy",
-                   "pi_linear_scratch_bytes", "pi_linear_forward")
+                   "pi_linear_scratch_bytes", "pi_linear_scratch_bytes_upto", "pi_linear_forward")
 
 _vp, _i32, _i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
@@ -39,6 +39,7 @@ def _declare() -> None:
                 pi_linear_create=[p(LinearDesc), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp, p(_vp)],
                 pi_linear_destroy=[_vp],
                 pi_linear_scratch_bytes=[_vp, _i32, p(ctypes.c_size_t)],
+                pi_linear_scratch_bytes_upto=[_vp, _i32, p(ctypes.c_size_t)],
                 pi_linear_forward=[_vp, p(LinearArgs), _vp])
     for name, args in sigs.items():
         fn = getattr(LIB, name)
@@ -173,12 +174,14 @@ class Linear:
             with torch.cuda.device(self.device.index):
                 check(fn(*args))
 
-    def scratch_bytes(self, rows) -> int:
-        """Bytes of scratch that forward takes for `rows` rows."""
+    def scratch_bytes(self, rows, upto=False) -> int:
+        """Bytes of scratch that forward takes for `rows` rows.  More rows may take less (their columns are split into fewer
+        ranges): with `upto`, the most that any number of rows up to `rows` takes, for a scratch that serves them all."""
         if rows >> 31:
             raise _invalid(f"rows={rows} does not fit in 32 bits")
         out = ctypes.c_size_t(0)
-        check(LIB.pi_linear_scratch_bytes(self._live(), rows, _byref(out)))
+        size = LIB.pi_linear_scratch_bytes_upto if upto else LIB.pi_linear_scratch_bytes
+        check(size(self._live(), rows, _byref(out)))
         return int(out.value)
 
     def _live(self):
@@ -189,7 +192,8 @@ class Linear:
     def forward(self, x, y, add=None, scratch=None, stream=None) -> None:
         """y [rows][d_out] = x [rows][d_in] W^T + bias + add [rows][d_out].  Rows may be strided (x's by a multiple of
         8 elements), the innermost dimension is contiguous.  y may be add itself.  scratch: scratch_bytes(rows) bytes
-        (0 up to 64 rows), made here unless given."""
+        (0 up to 64 rows), made here unless given; with less, down to what one range of columns takes, a call that would split
+        its columns is slower."""
         d, handle = self.desc, self._live()
         xs = self._rows(x, "x", d.d_in)
         rows = x.shape[0]

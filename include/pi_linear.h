@@ -40,7 +40,7 @@
 extern "C" {
 #endif
 
-#define PI_LINEAR_ABI_VERSION 1
+#define PI_LINEAR_ABI_VERSION 2
 
 typedef enum pi_linear_act { PI_LINEAR_F16 = 0, PI_LINEAR_BF16 = 1 } pi_linear_act;
 
@@ -58,7 +58,7 @@ typedef struct pi_linear_args {
   int64_t x_stride;   /* from row to row, in elements: a multiple of 8 up to 2^23 (looked at for several rows) */
   int64_t add_stride; /* in elements                                                        */
   int64_t y_stride;   /* in elements, at least d_out                                        */
-  void* scratch;      /* pi_linear_scratch_bytes, 16-byte aligned; not looked at where that is 0 */
+  void* scratch;      /* pi_linear_scratch_bytes, 16-byte aligned, or less: see there; not looked at where that is 0 */
   size_t scratch_bytes;
   int32_t rows;       /* 0 to 2^24; 0 enqueues nothing                                      */
 } pi_linear_args;
@@ -81,8 +81,17 @@ pi_status pi_linear_create(const pi_linear_desc* desc, const void* w, const void
 /* Release the handle (host memory only). */
 pi_status pi_linear_destroy(pi_linear* h);
 
-/* Bytes of scratch a call with as many rows takes: 0 up to 64 rows.  Host only. */
+/*
+ * Bytes of scratch a call with as many rows takes: 0 up to 64 rows.  Host only.
+ *
+ * Where the rows alone are too little work for the card, columns are split into up to 8 ranges, each with fp32 sums in the scratch,
+ * so a call with more rows may take less.  A call makes as many ranges as its scratch holds, so what a number of rows takes is
+ * enough for fewer rows too, if slower where these would be split (and with other last bits: the ranges' sums are joined).
+ */
 pi_status pi_linear_scratch_bytes(const pi_linear* h, int32_t rows, size_t* bytes);
+
+/* The most that pi_linear_scratch_bytes says for any number of rows up to `rows`: no call of these is slower for it. */
+pi_status pi_linear_scratch_bytes_upto(const pi_linear* h, int32_t rows, size_t* bytes);
 
 /* y = W x + bias + add for every row. */
 pi_status pi_linear_forward(pi_linear* h, const pi_linear_args* args, void* stream);

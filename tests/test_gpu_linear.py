@@ -325,3 +325,27 @@ def test_small_scales_beside_large_ones(rows, act):
     want = want.clamp(-float(torch.finfo(DT[act]).max), float(torch.finfo(DT[act]).max))
     err = (y.cpu().double().clamp(-float(torch.finfo(DT[act]).max), float(torch.finfo(DT[act]).max)) - want).abs()
     assert bool((err <= EPS[act] * want.abs() + TINY[act] + 2.0 ** -22 * 8 * x.max()).all())
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [65, 130, 300])
+def test_scratch_of_other_calls(rows, act):
+    """Columns are split into as many ranges as the scratch holds: that of more rows, which may take less, is enough."""
+    announce(f"linear scratch of other calls {rows} {act}")
+    r = Rig(4096, 200, act, bias=True, seed=rows)
+    x, add = r.x(rows), torch.from_numpy(r.rng.standard_normal((rows, 200))).to(DT[act])
+    need, whole = r.m.scratch_bytes(rows), r.m.scratch_bytes(60000, upto=True)
+    least = 0 if act == "f16" else -(-rows * 8192 // 256) * 256 + -(-rows * 4 // 256) * 256
+    assert r.m.scratch_bytes(60000) < need if act == "f16" else least < need < whole
+    sums = rows * 200 * 4
+    for size in sorted({least, least + sums, least + 2 * sums, least + 2 * sums + 300, least + 5 * sums, need - 1, need, need + 999}):
+        scratch = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+        y = torch.full((rows, 200), float("nan"), dtype=DT[act], device="cuda")
+        r.m.forward(x.cuda(), y, add.cuda(), scratch=scratch[:size])
+        torch.cuda.synchronize()
+        r.check(x, y, add)
+        assert bool((scratch[size:] == 77).all())
+    if act == "f16":
+        big = torch.empty(r.m.scratch_bytes(60000), dtype=torch.uint8, device="cuda")
+        r.m.forward(x.cuda(), y, add.cuda(), scratch=big)
+        r.check(x, y, add)

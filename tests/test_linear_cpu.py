@@ -166,3 +166,31 @@ def test_weights_are_checked():
     _rejects(lambda: pi.Linear(w, None), "scales must be a torch tensor")
     _rejects(lambda: pi.Linear(w[0], s), "w must be")
     _rejects(lambda: pi.Linear(w[:, :8], s), "d_in=16 must be")
+
+
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+@pytest.mark.parametrize("d_in, d_out", [(4096, 12288), (8192, 8192), (512, 100), (11008, 4096), (64, 8), (2048, 40000)])
+def test_a_scratch_for_all_numbers_of_rows(d_in, d_out, act):
+    """upto is the most of all smaller calls, and no call of fewer rows needs more than a larger one's, to be answered at all."""
+    h, out, most, least = _Handle(d_in, d_out, act), ctypes.c_size_t(0), 0, 0
+    for rows in list(range(60, 700)) + list(range(700, 9000, 37)):
+        assert pi.LIB.pi_linear_scratch_bytes(ctypes.byref(h.raw), rows, ctypes.byref(out)) == 0
+        most = max(most, out.value)
+        if rows > 64 and act == "bf16":     # fp16 rows and their factors, as one range of columns needs them
+            need = -(-rows * d_in * 2 // 256) * 256 + -(-rows * 4 // 256) * 256
+            assert least <= need <= out.value
+            least = need
+            assert h.forward(rows=rows, x_stride=d_in, y_stride=d_out, scratch=FAKE, scratch_bytes=need - 1) == 2
+            assert str(need) in pi.last_error()
+        before = out.value
+        assert pi.LIB.pi_linear_scratch_bytes_upto(ctypes.byref(h.raw), rows, ctypes.byref(out)) == 0
+        assert before <= out.value
+        if rows < 700:
+            assert out.value == most
+    m = _closed()
+    m.handle = ctypes.pointer(h.raw)
+    assert m.scratch_bytes(rows, upto=True) == out.value
+    m.handle = None
+    for bad in ((None, 1, out), (ctypes.byref(h.raw), -1, out), (ctypes.byref(h.raw), (1 << 24) + 1, out)):
+        assert pi.LIB.pi_linear_scratch_bytes_upto(bad[0], bad[1], ctypes.byref(out)) == 1
+    assert pi.LIB.pi_linear_scratch_bytes_upto(ctypes.byref(h.raw), 1, None) == 1
