@@ -235,6 +235,18 @@ size_t state_bytes(const pi_kv_desc& d, int32_t rows) {
   return (size_t)pik::shared_parts(rows, d.heads / d.kv_heads, d.kv_heads, 1) * rows * d.heads * (d.head_dim + 4) * sizeof(float);
 }
 
+// The most that state_bytes() says for any number of rows up to `rows`: parts grow fewer from tile to tile of 128 rows of a
+// cached head, so it is most at a tile's last row.
+size_t state_bytes_upto(const pi_kv_desc& d, int32_t rows) {
+  const int group = d.heads / d.kv_heads;
+  size_t most = state_bytes(d, rows);
+  for (long long tiles = 1; pik::shared_tiles(rows, group, 1) > tiles && tiles * d.kv_heads <= pik::kSharedParts / 2; ++tiles) {
+    const int32_t last = (int32_t)(tiles * 128 / group);
+    if (last > 0 && last < rows) most = std::max(most, state_bytes(d, last));
+  }
+  return most;
+}
+
 void fill_attend(pik::KvAttendArgs& a, const pi_kv* h, int32_t layer, const pi_kv_attend_args* args,
                  const pi_kv_batch* batch) {
   a.c = view_of(h, layer, batch);
@@ -368,7 +380,7 @@ pi_status pi_kv_state_bytes(const pi_kv* h, int32_t rows, size_t* bytes) {
   if (h == nullptr) return fail(PI_ERR_INVALID, "handle is NULL");
   if (bytes == nullptr) return fail(PI_ERR_INVALID, "bytes is NULL");
   if (rows < 0 || rows > kMaxRows) return fail(PI_ERR_INVALID, "rows=%d must lie in [0, %d]", rows, kMaxRows);
-  *bytes = state_bytes(h->desc, rows);
+  *bytes = state_bytes_upto(h->desc, rows);
   return ok();
 }
 

@@ -418,7 +418,7 @@ class KVCache:
                   self._stream(stream, (seqs, starts, groups, plan)))
 
     def state_floats(self, rows) -> int:
-        """Elements of the fp32 scratch that attend_shared takes for `rows` rows."""
+        """Elements of the fp32 scratch that attend_shared takes for any number of rows up to `rows`."""
         if rows >> 31:
             _in32(rows=rows)
         out = ctypes.c_size_t(0)

@@ -164,7 +164,7 @@ typedef struct pi_kv_rotate_args {
 typedef struct pi_kv_shared_args {
   const int32_t* groups; /* [n_groups + 1]                                                     */
   const int32_t* plan;   /* [n_groups + n], as pi_kv_share leaves it                           */
-  void* state;           /* scratch of the call: pi_kv_state_bytes, 16-byte aligned            */
+  void* state;           /* scratch of the call: pi_kv_state_bytes of its rows or more, 16-byte aligned */
   size_t state_bytes;
   int32_t n_groups;      /* 1 .. n                                                             */
   int32_t max_rows;      /* at least the largest count of tokens (rows) of a group             */
@@ -231,7 +231,7 @@ pi_status pi_kv_attend(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, c
 pi_status pi_kv_share(pi_kv* h, const pi_kv_batch* batch, const int32_t* groups, int32_t n_groups, int32_t* plan,
                       void* stream);
 
-/* Bytes of scratch that pi_kv_attend_shared takes for `rows` rows.  Host only. */
+/* Bytes of scratch that pi_kv_attend_shared takes for any number of rows up to `rows`.  Host only. */
 pi_status pi_kv_state_bytes(const pi_kv* h, int32_t rows, size_t* bytes);
 
 /*

@@ -136,3 +136,17 @@ def test_no_block_past_the_table(tmp_path):
     subprocess.run([hipcc(), "--cuda-host-only", "-std=c++17", "-O1", "-I", CSRC, str(tmp_path / "spans.hip"), "-o",
                     str(tmp_path / "spans")], check=True, timeout=100)
     assert subprocess.run([str(tmp_path / "spans")], timeout=20).returncode == 0
+
+
+@pytest.mark.parametrize("heads, kv_heads, dim", [(8, 2, 64), (64, 8, 128), (128, 8, 64), (32, 32, 128), (1024, 1, 64), (300, 300, 64)])
+def test_a_state_for_all_numbers_of_rows(heads, kv_heads, dim):
+    """What a number of rows is said to take serves fewer rows too, whose shared tokens may be taken in more parts."""
+    raw = _Raw(pi.kv_desc(heads, kv_heads, dim, 9, 64, 3, 4), kvc.KvBuffers(*[FAKE] * 9), FAKE)
+    out, least = ctypes.c_size_t(0), 0
+    group = heads // kv_heads
+    for rows in range(0, 3000):
+        items = (rows * group + 127) // 128 * kv_heads
+        parts = 512 // items if 0 < items <= 256 else 1
+        assert pi.LIB.pi_kv_state_bytes(ctypes.byref(raw), rows, ctypes.byref(out)) == 0
+        least = max(least, parts * rows * heads * (dim + 4) * 4)     # of one group's sequences
+        assert out.value == least, rows
