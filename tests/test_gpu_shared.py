@@ -400,3 +400,24 @@ def test_plan_past_a_full_sequence(new):
         f.compare(q[:2 * new], out[:2 * new], lse[:2 * new], [0, new, 2 * new], [0, 1], 0, 0, None)
         for name, t in before.items():
             assert torch.equal(t, getattr(f.cache, name))
+
+
+@pytest.mark.parametrize("act, code", [("f16", "e4m3"), ("bf16", "int8"), ("bf16", "e4m3"), ("f16", "int8")])
+@pytest.mark.parametrize("groups, members, new, heads", [
+    (1, 3, 5, (8, 1, 128)),     # shared tokens in parts, joined by a launch: 120 rows of a head, 40 own
+    (2, 4, 9, (16, 2, 128)),    # the same with several heads, 72 own rows: the kernel of many rows behind it
+    (1, 5, 3, (8, 1, 128)),     # 24 own rows, which join the parts themselves
+    (2, 2, 4, (8, 2, 128)),     # 32 and 16 rows
+    (1, 2, 2, (16, 2, 128)),    # 32 rows, and 16 own
+    (4, 2, 6, (64, 8, 128)),    # 48 own rows of 64 items
+    (8, 2, 3, (64, 8, 128)),    # 48 rows of 64 groups' heads, and 24 own
+    (8, 4, 2, (64, 8, 128)),    # 64 rows, and 16 own
+    (8, 1, 8, (64, 8, 128))])   # lone sequences: 64 rows, nothing shared
+def test_wide_heads(groups, members, new, heads, act, code):
+    """128 dims, each number of row tiles on both sides, over prefixes that are cut."""
+    announce(f"shared wide {groups} x {members}, {new} new, {heads} {act} {code}")
+    f = Family([2500 - 300 * g for g in range(groups)], [[new + (13 * i + 5 * g) % 90 for i in range(members)] for g in range(groups)],
+               *heads, 64, act, code, seed=new)
+    f.step([new] * f.n)
+    if new > 2:
+        f.step([1 + (i % new) for i in range(f.n - 1)] + [new])
