@@ -97,7 +97,8 @@ pi_status check_rope(const pi_rope_desc* d) {
     return fail(PI_ERR_INVALID, "layout=%d is not a pi_rope_layout", d->layout);
   if (d->scaling < PI_ROPE_NONE || d->scaling > PI_ROPE_BANDS)
     return fail(PI_ERR_INVALID, "scaling=%d is not a pi_rope_scaling", d->scaling);
-  if (!(d->gain > 0) || !std::isfinite((float)d->gain)) return fail(PI_ERR_INVALID, "gain=%g must be positive and finite", d->gain);
+  if (!((float)d->gain > 0) || !std::isfinite((float)d->gain))
+    return fail(PI_ERR_INVALID, "gain=%g must be positive and finite in fp32", d->gain);
   if (d->freqs != nullptr) {
     if (d->scaling != PI_ROPE_NONE) return fail(PI_ERR_INVALID, "freqs are given: scaling must be PI_ROPE_NONE");
     for (int i = 0; i < d->rot_dims / 2; ++i)

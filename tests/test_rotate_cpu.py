@@ -144,3 +144,12 @@ def test_binding(change, needle):
     with pytest.raises(pi.PiError) as e:
         _cache().rotate(**_args(**change))
     assert e.value.status == 1 and needle in str(e.value), str(e.value)
+
+
+@pytest.mark.parametrize("gain", [1e-50, -1e-50, -1.0, 1e39, math.nan])
+def test_gains_outside_fp32(gain):
+    """A gain that fp32 holds as 0 would clear every turned dim."""
+    with pytest.raises(pi.PiError) as e:
+        pi.Rope(64, gain=gain)
+    assert e.value.status == 1 and "gain" in str(e.value)
+    assert pi.Rope(64, gain=1e-38).desc.gain == 1e-38
