@@ -88,7 +88,8 @@ hipError_t launch_kv_tile_shared(int act, int code, int mode, const KvSharedArgs
 // Few rows of a cached head (max_new * group up to kStepRows): items (sequences times cached heads) in pieces, one
 // workgroup each, see kv_step.h.  S is at least kStepGrain blocks.
 // (Behind shared tokens items are short, and a part to join costs more than some 24 blocks: two layers of 64 sequences on
-// 4096 shared tokens, 8 cached heads, 108 us with 32, 123 with 8.)
+// 4096 shared tokens, 8 cached heads, 108 us with 32, 123 with 8.  Few items of long sequences lose little: 4 of 2000 own
+// tokens, 8 cached heads, 16.6 us in 64 pieces, where whole sequences take 15.1 by pieces of 8.)
 constexpr int kStepRows = 64, kStepGrain = 8, kOwnGrain = 32;
 // tiles: 16-row tiles a wave holds.  One to four workgroups a compute unit, by the registers these take.  Eight
 // waves instead of four where 33 to 64 rows have 64 dims: half as many parts to join (four tokens over 100003, 16

@@ -4,16 +4,18 @@
 // codes of a word become two operands of a matrix instruction with one `and` and one `or` (the word is rotated by
 // four bits from pair to pair), and no conversion.
 //
-// Up to 64 rows are bound by reading the codes and x, and their sums are exact but for fp32's own rounding: the 24 is taken
+// Up to 64 rows are bound by reading the codes and x, and nothing is rounded but sums in fp32: the 24 is taken
 // off by the accumulator that a product begins with, c = -24 sum x over the group, itself a product of the same x
 // with a constant; each group of 32 columns is one 16x16x32 product, and its sum, times the scale, is added in fp32.
+// These sums round at the size of 24 x to 31 x, where q x has up to 8 x: up to 2600 * 2^-24 of a group's sum of |x|.
 //
 // More than 64 rows are bound by issue: on this hardware a vector ALU instruction runs beside a matrix instruction only in part
 // (a 16x16x32 one and n others take 15.6 + 3.7 n cycles together, a 32x32x16 one, twice the work, 19 + 3.9 n), and an
 // fp32 multiply-add for each output and group alone takes as many cycles as the product itself (2000 rows 4096 -> 12288:
 // 328 us).  So there code times scale is an fp16 operand, rounded to half a step of 2^-11, no more than an fp16 y itself
 // is, and the sums stay in 32x32x16 products.  bf16 rows are made fp16 for this, each by a power of two of its own, in the
-// caller's scratch: what is lost lies 2^-39 below a row's largest.
+// caller's scratch: what is lost lies 2^-39 below a row's largest.  On measured weights an fp16 y is off by 2.7e-4
+// (relative, root mean square) where 64 rows' sums leave it at the 2.1e-4 of its own rounding, and a bf16 y by 1.7e-3 both ways.
 //
 // Measured (codes and scales read once at 6.99 TB/s; products at a library's 1166 to 1223 TFLOP/s): 1 row 8192 -> 10240 10.0 us
 // (6.8); 16 rows 8192 -> 8192 11.3 to 12.4 (5.5); 64 rows 7168 -> 21504 45 to 47 (12.9; products 16.1), where each workgroup reads all of x
@@ -649,9 +651,11 @@ hipError_t linear_any(const LinearArgs& a, hipStream_t s) {
   if (a.rows <= 16) return rows_go<ACT, 1, 2, 8, 4, 2>(a, s);
   if (a.rows <= 32) return rows_go<ACT, 2, 2, 8, 2, 1>(a, s);
   if (a.rows <= kExactRows) {
-    // the registers and LDS of eight waves fill a compute unit, and so the card is filled once: 64 rows 8192 -> 8192, 512
-    // tiles, 23.5 us by two tiles and eight waves, 24.7 by four waves, 31.5 by three tiles; 7168 -> 21504, 1344 tiles,
-    // 47.3 us by three tiles and four waves, 51.8 by two, 56.4 by two and eight waves
+    // the registers and LDS of eight waves fill a compute unit: 256 workgroups of eight waves, or 512 of four, are at work
+    // at once.  64 rows, us by two tiles and eight waves, two and four, three and four: 8192 columns, 512 tiles 24.0, 25.0,
+    // 30.0; 640 tiles 41.2, 37.8, 30.6; 768 tiles 41.8, 38.4, 32.2; 1024 tiles 46, 42.0, 49.2; 1792 tiles 85, 74.8, 75.0;
+    // 7168 columns, 1280 tiles 57.5, 51.6, 46.2; 1344 tiles 57.9, 51.8, 46.4; 1536 tiles 61, 55.0, 49.2.  (Up to 768 tiles
+    // three would be a workgroup for each compute unit.)
     if (a.tiles <= 512) return rows_go<ACT, 4, 2, 8, 2, 1>(a, s);
     return a.tiles <= 1024 ? rows_go<ACT, 4, 2, 4, 2, 1>(a, s) : rows_go<ACT, 4, 3, 4, 2, 1>(a, s);
   }

@@ -4,7 +4,8 @@
 //
 // for the pairs (a, b) of the first `rot` dims, t = position times the pair's frequency.  Frequencies are whole
 // numbers of 2^-64 turns, so that position times frequency, taken modulo one turn, is one exact integer product however
-// far the position is; its upper 32 bits go to the sine and cosine, which this hardware takes in turns.
+// far the position is; its upper 32 bits go to the sine and cosine, which this hardware takes in turns, as fp32: to 2^-26
+// of a turn.
 //
 // A lane holds 8 dims of a head.  A wave takes one token and PER times as many heads as fit in it, so that their
 // angles are worked out once.

@@ -429,7 +429,8 @@ class KVCache:
                       stream=None) -> None:
         """attend (whole sequences, no window) for groups of sequences that begin with the same pages: what `plan` (share)
         says a group shares is read and multiplied once for all of its rows.  max_rows: at least the largest count of
-        rows of a group.  state: fp32 scratch of state_floats(rows) elements, made here unless given."""
+        rows of a group.  state: fp32 scratch of state_floats(rows) elements, made here unless given.  For long prompts and many
+        sequences: where little is shared attend is faster (pi_kv.h says from where on this one is)."""
         d = self.desc
         n = self._ids(seqs, "seqs")
         self._ids(starts, "starts", n + 1)

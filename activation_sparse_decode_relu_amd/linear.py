@@ -79,6 +79,10 @@ class Linear:
 
     The weights are laid out once, here (`packed`, made unless given); w and scales may then be let go of.  Calls may
     run at the same time on several streams.
+
+    Up to 64 rows sums are rounded in fp32 alone.  More rows take code times scale rounded to fp16, so that y is off by up to
+    2^-11 of sum |w x| before its own rounding: call with 64 rows at a time where that is too much.  (pi_linear.h has the
+    bounds, and what becomes of infinities.)
     """
 
     def __init__(self, w, scales, act_dtype="f16", bias=None, packed=None, stream=None):
@@ -191,9 +195,9 @@ class Linear:
 
     def forward(self, x, y, add=None, scratch=None, stream=None) -> None:
         """y [rows][d_out] = x [rows][d_in] W^T + bias + add [rows][d_out].  Rows may be strided (x's by a multiple of
-        8 elements), the innermost dimension is contiguous.  y may be add itself.  scratch: scratch_bytes(rows) bytes
-        (0 up to 64 rows), made here unless given; with less, down to what one range of columns takes, a call that would split
-        its columns is slower."""
+        8 elements), the innermost dimension is contiguous.  y may be add itself, and else overlaps neither x nor add.
+        scratch: scratch_bytes(rows) bytes (0 up to 64 rows), made here unless given; with less, down to what one range of
+        columns takes, a call that would split its columns is slower."""
         d, handle = self.desc, self._live()
         xs = self._rows(x, "x", d.d_in)
         rows = x.shape[0]

@@ -9,7 +9,8 @@ FFN) is captured once and replayed.  Then the second half of the sequences gives
 is compacted, as a beam search or a server does between steps.
 
 --q4 holds the attention's projections in 4 bits; --rope turns queries and keys by their positions and normalises them;
---beams B runs B sequences on each prompt, which the attention then reads once for all of them.
+--beams B runs B sequences on each prompt, which the attention then reads once for all of them (which is worth its second
+launch for long prompts and many beams, see pi_kv.h).
 """
 
 import argparse

@@ -238,6 +238,11 @@ pi_status pi_kv_state_bytes(const pi_kv* h, int32_t rows, size_t* bytes);
  * pi_kv_attend for groups: the same results up to the order of sums, but the first plan[g] tokens of a group are read
  * once, from its first sequence's pages, for all rows of the group.  Whole sequences: window and sinks are 0.  A plan
  * that was not made for these sequences gives rows that mean nothing (and touches no other memory).
+ *
+ * It makes two launches where pi_kv_attend makes one, and leaves states between them: some 10 us more a call.  pi_kv_attend finds
+ * what sequences share in the caches after the first of them, so this one is the faster only from some 300 MB on of codes
+ * that it spares: (sequences of a group - 1) * shared tokens * kv_heads * 2 * head_dim bytes, summed; and from some four times as
+ * much where each brings several tokens of grouped heads.
  */
 pi_status pi_kv_attend_shared(pi_kv* h, int32_t layer, const pi_kv_attend_args* args, const pi_kv_shared_args* shared,
                               const pi_kv_batch* batch, void* stream);
@@ -263,7 +268,9 @@ pi_status pi_rope_freqs(const pi_rope* rope, double* freqs);
  * Queries and keys as append and attend take them: with a norm, each head x becomes x / sqrt(mean x^2 + eps) * norm;
  * then its first dims turn by their token's position, lens[s] - count + j for row starts[i] + j of s = seqs[i], as in
  * pi_kv_attend (lens counts the tokens already), or the given one.  In fp32 (a head's sum of squares has to be in
- * its range), rounded once; angles are exact to 2^-32 of a turn at any position.  Rows of no sequence stay as they are.
+ * its range), rounded once; with the frequencies that pi_rope_freqs gives, angles are off by up to 2^-26 of a turn at any
+ * position, and their sines and cosines by up to 2^-20.  Rows of no sequence stay as they are; those of a sequence
+ * that is out of range mean nothing.
  */
 pi_status pi_kv_rotate(pi_kv* h, const pi_rope* rope, const pi_kv_rotate_args* args, const pi_kv_batch* batch,
                        void* stream);

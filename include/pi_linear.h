@@ -23,13 +23,16 @@
  * - Ownership: the caller allocates all device memory; a handle borrows it until pi_linear_destroy.
  * - Streams: calls only enqueue on `stream`.  A handle has no workspace: its calls may run at the same time, each
  *   with a scratch of its own.
- * - Up to 64 rows: products of whole numbers and activations are summed in fp32 by groups of 32, and the groups'
- *   sums, times their scales, in fp32.  More rows: code times scale is rounded to fp16 (half a step of 2^-11), and
- *   so are bf16 rows, relative to their largest (exact down to 2^-29 of it, and 2^-39 of it lost at most); products
- *   are summed in fp32.  y is rounded once.  A row's result depends on its own x, and, in its last bits, on the number
- *   of rows of the call; it does not depend on the order in which workgroups run.
- * - A row of x that holds an infinity, a NaN, or (bf16) a magnitude of 2^118 and more may come out as NaN, other
- *   rows are not touched by it.
+ * - Up to 64 rows: products of the whole numbers 24 + q with x are summed in fp32 by groups of 32, from -24 times the sum of
+ *   x on, and the groups' sums, times their scales, in fp32.  So a group is off by up to 2^-12 of its sum of |x|, times its
+ *   scale, also by an x whose q is 0.
+ * - More than 64 rows give fewer bits: code times scale is rounded to fp16 (half a step, 2^-11 of it), so y is off by up to
+ *   2^-11 sum |w x| before its own rounding, and bf16 rows are made fp16 relative to their largest (exact down to 2^-29 of it,
+ *   and 2^-39 of it lost at most).  Products are summed in fp32.  Where 64 rows' accuracy is needed for more, call with 64.
+ * - y is rounded once.  A row's result depends on its own x and on the number of rows of the call: as said, beyond 64, and in
+ *   its last bits otherwise.  It does not depend on the order in which workgroups run.
+ * - A row of x that holds a NaN, an infinity, or (bf16) a magnitude of 2^118 and more may come out as NaN, also where the
+ *   sum would be infinite (up to 64 rows an infinity always does), other rows are not touched by it.
  */
 #ifndef PI_LINEAR_H
 #define PI_LINEAR_H
@@ -50,7 +53,7 @@ typedef struct pi_linear_desc {
   int32_t act_dtype; /* pi_linear_act: type of x, add and y */
 } pi_linear_desc;
 
-/* Rows of a call: y may be add itself, and else overlaps neither x nor add. */
+/* Rows of a call: y may be add itself, and else overlaps neither x nor add (which is not looked at). */
 typedef struct pi_linear_args {
   const void* x;      /* [rows][d_in], 16-byte aligned                                      */
   const void* add;    /* [rows][d_out] or NULL                                              */
@@ -84,9 +87,10 @@ pi_status pi_linear_destroy(pi_linear* h);
 /*
  * Bytes of scratch a call with as many rows takes: 0 up to 64 rows.  Host only.
  *
- * Where the rows alone are too little work for the card, columns are split into up to 8 ranges, each with fp32 sums in the scratch,
- * so a call with more rows may take less.  A call makes as many ranges as its scratch holds, so what a number of rows takes is
- * enough for fewer rows too, if slower where these would be split (and with other last bits: the ranges' sums are joined).
+ * Where the rows alone are too little work for the card, columns are split into up to 8 ranges, each with fp32 sums in the
+ * scratch, so a call with more rows may take less.  A call makes as many ranges as its scratch holds, so what a number of
+ * rows takes is enough for fewer rows too, if slower where these would be split (and with other last bits: the ranges' sums
+ * are joined).
  */
 pi_status pi_linear_scratch_bytes(const pi_linear* h, int32_t rows, size_t* bytes);
 
